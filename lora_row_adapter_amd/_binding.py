@@ -86,6 +86,27 @@ class _CQWeight(ctypes.Structure):
     ]
 
 
+class _CMx(ctypes.Structure):
+    _fields_ = [
+        ("format", ctypes.c_int32),
+        ("q", ctypes.c_void_p),
+        ("ldq", ctypes.c_int64),
+        ("scales", ctypes.c_void_p),
+        ("lds", ctypes.c_int64),
+    ]
+
+
+class _CNorm(ctypes.Structure):
+    _fields_ = [
+        ("weight", ctypes.c_void_p),
+        ("eps", ctypes.c_float),
+        ("residual", ctypes.c_void_p),
+        ("ldr", ctypes.c_int64),
+        ("residual_out", ctypes.c_void_p),
+        ("ldro", ctypes.c_int64),
+    ]
+
+
 class _CPoolDesc(ctypes.Structure):
     _fields_ = [
         ("pool", ctypes.c_void_p),
@@ -163,6 +184,20 @@ def load_library():
     lib.lora_linear_sliced_q.argtypes = [i64, i64, p, i64, pqw, i32, ctypes.POINTER(_CSlice), p, p,
                                          i64, p, sz, i32, u32, p]
     lib.lora_linear_sliced_q.restype = i32
+    pmx, pno = ctypes.POINTER(_CMx), ctypes.POINTER(_CNorm)
+    lib.lora_mx_quantize.argtypes = [i32, i64, i64, p, i64, pmx, p]
+    lib.lora_mx_quantize.restype = i32
+    lib.lora_mx_dequantize.argtypes = [i32, i64, i64, pmx, p, i64, p]
+    lib.lora_mx_dequantize.restype = i32
+    lib.lora_rmsnorm.argtypes = [i32, i64, i64, p, i64, pno, p, i64, pmx, p]
+    lib.lora_rmsnorm.restype = i32
+    lib.lora_gemm_mx.argtypes = [i64, i64, i64, pmx, pmx, p, i64, p]
+    lib.lora_gemm_mx.restype = i32
+    lib.lora_workspace_bytes_sliced_mx.argtypes = [i64, i64, i32, i32, psl]
+    lib.lora_workspace_bytes_sliced_mx.restype = sz
+    lib.lora_linear_sliced_mx.argtypes = [i64, i64, p, i64, pno, i32, pmx, i32, psl, p, p, i64, p,
+                                          sz, i32, u32, p]
+    lib.lora_linear_sliced_mx.restype = i32
     lib.lora_merge.argtypes = [i32, i64, i64, p, i64, pad, i32, p, ctypes.c_float, p, i64, p]
     lib.lora_merge.restype = i32
     lib.lora_translate.argtypes = [pad, p, p, i64, p, p]
@@ -716,6 +751,225 @@ def lora_linear_sliced_q(x: torch.Tensor, W: QWeight, slices, adapter_ids: torch
                                   _dev(workspace, "workspace"), workspace.numel(), int(path),
                                   int(flags), _stream_ptr(stream))
     _check(st, "lora_linear_sliced_q")
+    return y
+
+
+MX_FP8, MX_FP4 = 1, 2
+
+
+def _on(device: torch.device, stream, fn, what: str, *args) -> None:
+    """fn(*args, stream) with `device` current (a stream belongs to its
+    device); by default on that device's current stream."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        status = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, stream.cuda_stream)
+    if status != 0:
+        raise LoraError(status, what)
+
+
+def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype, device):
+    """(pointer, leading dimension) of a row-major [rows, cols] tensor of
+    this dtype on this device."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError("%s must be [%d, %d]" % (name, rows, cols))
+    if t.device != device or not t.is_cuda:
+        raise ValueError("%s must be a tensor on %s" % (name, device))
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+class MX:
+    """A microscaled matrix [rows, k] (include/lora_mx.h, lora_mx_t): codes
+    `q`, uint8 [rows, >= ceil(k / 32) * 32 (MX_FP8) or * 16 (MX_FP4)], and a
+    scale byte per 32 elements, uint8 [rows, >= ceil(k / 32)]."""
+
+    __slots__ = ("fmt", "q", "scales", "k", "rows", "_c", "_ref")
+
+    def __init__(self, fmt: int, q: torch.Tensor, scales: torch.Tensor, k: int):
+        if fmt not in (MX_FP8, MX_FP4):
+            raise ValueError("fmt must be MX_FP8 or MX_FP4")
+        if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+            raise TypeError("q and scales must be uint8")
+        if not q.is_cuda or q.device != scales.device:
+            raise ValueError("q and scales must be tensors on one device")
+        k = int(k)
+        nb = (k + 31) // 32
+        width = nb * (32 if fmt == MX_FP8 else 16)
+        if q.dim() != 2 or scales.dim() != 2 or q.shape[0] != scales.shape[0]:
+            raise ValueError("q and scales must be 2-D with one row per row of the matrix")
+        if k < 1 or q.shape[1] < width or scales.shape[1] < nb:
+            raise ValueError("k = %d needs %d bytes of codes and %d scales a row" % (k, width, nb))
+        if q.stride(1) != 1 or scales.stride(1) != 1 and nb > 1:
+            raise ValueError("q and scales must have unit stride along their last dimension")
+        self.fmt, self.q, self.scales, self.k, self.rows = int(fmt), q, scales, k, q.shape[0]
+        c = _CMx()
+        c.format = self.fmt
+        c.q = q.data_ptr()
+        c.scales = scales.data_ptr()
+        # a single row may have any stride
+        c.ldq = q.stride(0) if self.rows > 1 else width
+        c.lds = scales.stride(0) if self.rows > 1 else (nb + 3) // 4 * 4
+        self._c = c
+        self._ref = ctypes.byref(c)
+
+    @classmethod
+    def empty(cls, rows: int, k: int, fmt: int, device="cuda") -> "MX":
+        """Uninitialised storage with the least strides the library takes."""
+        nb = (int(k) + 31) // 32
+        q = torch.empty((rows, nb * (32 if fmt == MX_FP8 else 16)), dtype=torch.uint8, device=device)
+        return cls(fmt, q, torch.empty((rows, (nb + 3) // 4 * 4), dtype=torch.uint8, device=device), k)
+
+    @property
+    def device(self) -> torch.device:
+        return self.q.device
+
+    def ref(self):
+        return self._ref
+
+
+def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = None,
+                     stream=None) -> MX:
+    """Microscaled x (float32 or bfloat16 [M, k])."""
+    lib = load_library()
+    dt = _dtype_code(x)
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a 2-D device tensor")
+    M, k = x.shape
+    if out is None:
+        out = MX.empty(M, k, fmt, x.device)
+    elif out.fmt != fmt or out.rows != M or out.k != k or out.device != x.device:
+        raise ValueError("out must be a [%d, %d] matrix of this format on x's device" % (M, k))
+    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
+    _on(x.device, stream, lib.lora_mx_quantize, "lora_mx_quantize", dt, M, k, xp, ldx, out._ref)
+    return out
+
+
+def lora_mx_dequantize(q: MX, dtype: torch.dtype = torch.bfloat16,
+                       out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The values q stands for (float32 or bfloat16 [rows, k])."""
+    lib = load_library()
+    if dtype not in _DTYPES:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    if out is None:
+        out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)
+    yp, ldy = _matrix(out, "out", q.rows, q.k, dtype, q.device)
+    _on(q.device, stream, lib.lora_mx_dequantize, "lora_mx_dequantize", _DTYPES[dtype], q.rows, q.k,
+        q._ref, yp, ldy)
+    return out
+
+
+class Norm:
+    """A root-mean-square norm (lora_norm_t): weight [k], eps, and optionally
+    the residual that is added first and the tensor that receives the sum
+    (both [M, k]; the sum may go in place of x or of the residual)."""
+
+    def __init__(self, weight: torch.Tensor, eps: float = 1e-5,
+                 residual: Optional[torch.Tensor] = None,
+                 residual_out: Optional[torch.Tensor] = None):
+        self.weight, self.eps = weight, float(eps)
+        self.residual, self.residual_out = residual, residual_out
+
+    def c(self, x: torch.Tensor) -> _CNorm:
+        M, k = x.shape
+        w = self.weight
+        if w.dtype != x.dtype:
+            raise TypeError("the norm's weight must have x's dtype")
+        if w.dim() != 1 or w.shape[0] != k or w.device != x.device or not w.is_contiguous():
+            raise ValueError("the norm's weight must be a contiguous [%d] tensor on x's device" % k)
+        c = _CNorm()
+        c.weight = w.data_ptr()
+        c.eps = self.eps
+        if self.residual is not None:
+            c.residual, c.ldr = _matrix(self.residual, "residual", M, k, x.dtype, x.device)
+        if self.residual_out is not None:
+            c.residual_out, c.ldro = _matrix(self.residual_out, "residual_out", M, k, x.dtype, x.device)
+        return c
+
+
+def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
+                 yq: Optional[MX] = None, stream=None) -> Optional[torch.Tensor]:
+    """y = h / sqrt(mean(h^2) + eps) * weight with h = x + residual; yq takes
+    the normed rows microscaled.  y is made if neither is given."""
+    lib = load_library()
+    dt = _dtype_code(x)
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a 2-D device tensor")
+    M, k = x.shape
+    if y is None and yq is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
+    yp, ldy = (None, 0) if y is None else _matrix(y, "y", M, k, x.dtype, x.device)
+    if yq is not None and (yq.rows != M or yq.k != k or yq.device != x.device):
+        raise ValueError("yq must be a [%d, %d] matrix on x's device" % (M, k))
+    _on(x.device, stream, lib.lora_rmsnorm, "lora_rmsnorm", dt, M, k, xp, ldx,
+        ctypes.byref(norm.c(x)), yp, ldy, None if yq is None else yq._ref)
+    return y
+
+
+def lora_gemm_mx(x: MX, W: MX, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x W^T on microscaled operands (bfloat16 y [rows of x, rows of W])."""
+    lib = load_library()
+    if x.k != W.k or x.device != W.device:
+        raise ValueError("x and W differ in k or device")
+    if y is None:
+        y = torch.empty((x.rows, W.rows), dtype=torch.bfloat16, device=x.device)
+    yp, ldy = _matrix(y, "y", x.rows, W.rows, torch.bfloat16, x.device)
+    _on(x.device, stream, lib.lora_gemm_mx, "lora_gemm_mx", x.rows, x.k, W.rows, x._ref, W._ref, yp,
+        ldy)
+    return y
+
+
+def workspace_bytes_sliced_mx(max_rows: int, k: int, x_format: int, slices) -> int:
+    arr = _slice_array(slices)
+    n = load_library().lora_workspace_bytes_sliced_mx(int(max_rows), int(k), int(x_format),
+                                                      len(slices), arr)
+    if n == 0:
+        raise LoraError(1, "lora_workspace_bytes_sliced_mx")
+    return int(n)
+
+
+def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Tensor,
+                          x_format: int = MX_FP8, norm: Optional[Norm] = None,
+                          y: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, path: int = PATH_AUTO,
+                          flags: int = 0, stream=None) -> torch.Tensor:
+    """lora_linear_sliced over a microscaled stacked base weight: the rows of
+    x (normed first with a norm) meet W in x_format, the adapters in bf16."""
+    lib = load_library()
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("x must be a 2-D device tensor")
+    M, k = x.shape
+    d_total = sum(sl.d for sl in slices)
+    if W.rows != d_total or W.k != k or W.device != x.device:
+        raise ValueError("W must stack the slices' weights on x's device: [%d, %d] expected" % (d_total, k))
+    if y is None:
+        y = torch.empty((M, d_total), dtype=x.dtype, device=x.device)
+    if workspace is None:
+        workspace = torch.zeros(workspace_bytes_sliced_mx(M, k, x_format, slices), dtype=torch.uint8,
+                                device=x.device)
+    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
+    yp, ldy = _matrix(y, "y", M, d_total, x.dtype, x.device)
+    if adapter_ids.numel() != M:
+        raise ValueError("adapter_ids must have one entry per row")
+    for sl in slices:
+        ad = sl.adapters
+        if ad.kind == KIND_SLOTS and ad.A.dtype != x.dtype:
+            raise TypeError("adapter slots must have x's dtype")
+        if ad.kind == KIND_SLOTS and (ad.A.shape[2] != k or ad.B.shape[1] != sl.d):
+            raise ValueError("adapter slots must be A [S, R, %d] and B [S, %d, R]" % (k, sl.d))
+    _on(x.device, stream, lib.lora_linear_sliced_mx, "lora_linear_sliced_mx", M, k, xp, ldx,
+        None if norm is None else ctypes.byref(norm.c(x)), int(x_format), W._ref, len(slices),
+        _slice_array(slices), _dev(adapter_ids, "adapter_ids", torch.int32), yp, ldy,
+        _dev(workspace, "workspace"), workspace.numel(), int(path), int(flags))
     return y
 
 

@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblora_row.so")
 SOURCES = ["lora_api.cpp", "plan.hip", "gemm.hip", "lora_gather.hip", "lora_sgmv.hip",
-           "pool.hip", "pool_mgr.cpp", "merge.hip", "gemm_q.hip", "noalloc.hip"]
+           "pool.hip", "pool_mgr.cpp", "merge.hip", "gemm_q.hip", "noalloc.hip",
+           "mx.hip", "gemm_mx.hip", "mx_api.cpp"]
 ARCH = os.environ.get("LORA_ROW_ARCH", "gfx950")
 
 

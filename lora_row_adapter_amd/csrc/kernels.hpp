@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "lora_row.h"
+#include "lora_mx.h"
 #include "common.hpp"
 
 namespace lora {
@@ -175,6 +176,43 @@ struct QGemmArgs {
   int vec_store;
 };
 hipError_t launch_gemm_q(const QGemmArgs &a, hipStream_t st);
+// Microscaled operands (lora_mx.h).
+struct MxQuantArgs {
+  int32_t dtype;  // of x: 0 f32, 1 bf16
+  int32_t fmt;    // lora_mxformat_t
+  int64_t M, k;
+  const void *x;  // [M, ldx]: read by quantize, written by dequantize
+  int64_t ldx;
+  uint8_t *q;
+  int64_t ldq;
+  uint8_t *sc;
+  int64_t lds;
+};
+hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t st);
+hipError_t launch_mx_dequantize(const MxQuantArgs &a, hipStream_t st);
+struct RmsNormArgs {
+  int32_t dtype;
+  int32_t fmt;     // lora_mxformat_t, 0: no microscaled output
+  int64_t M, k;
+  const void *x, *res, *w;  // res may be nullptr
+  void *h, *y;              // each may be nullptr
+  int64_t ldx, ldr, ldh, ldy;
+  uint8_t *q, *sc;
+  int64_t ldq, lds;
+  float eps;
+};
+hipError_t launch_rmsnorm(const RmsNormArgs &a, hipStream_t st);
+// y = x W^T: x fp8 or fp4, W fp4, y bf16.
+struct MxGemmArgs {
+  int32_t xfmt;  // lora_mxformat_t of x
+  int32_t M, N, nb;  // nb: blocks of 32 per row
+  const uint8_t *x, *xs, *w, *wsc;
+  int64_t ldx, ldxs, ldw, ldws;  // bytes
+  uint16_t *y;
+  int64_t ldy;
+  int32_t tiles_m, tiles_n;
+};
+hipError_t launch_gemm_mx(const MxGemmArgs &a, hipStream_t st);
 hipError_t launch_shrink_gather(const LoraArgs &a, hipStream_t st);
 hipError_t launch_expand_gather(const LoraArgs &a, hipStream_t st);
 // A rows per stage the LDS-staged SGMV shrink takes for this launch (per
@@ -248,14 +286,36 @@ hipError_t launch_pool_fill(int32_t *p, int64_t n, int32_t v, hipStream_t st);
 hipError_t launch_pool_rows(const PoolRowsArgs &a, hipStream_t st);
 hipError_t launch_pool_pull(const PoolPullArgs &a, hipStream_t st);
 
-// The multi-slice layer behind lora_linear_sliced(_q) (the C ABI's types;
-// defined in lora_api.cpp).  self_contained: create no library resource --
+// Microscaled base of the layer: W, the format x is quantised to, and the
+// norm ahead of it (nullptr: none).
+struct MxBase {
+  const lora_mx_t *W;
+  int32_t x_format;
+  const lora_norm_t *norm;
+};
+// Host checks shared by the entry points (mx_api.cpp).
+lora_status_t check_mx(const lora_mx_t *m, int64_t rows, int64_t k);
+lora_status_t check_norm_in(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, int64_t ldx,
+                            const lora_norm_t *norm);
+lora_status_t check_norm(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, int64_t ldx,
+                         const lora_norm_t *norm, const void *y, int64_t ldy, const lora_mx_t *yq);
+lora_status_t check_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *W);
+// Part of a microscaled layer's workspace behind the plan regions of a chunk
+// of `rows` rows: the quantised rows and the normed rows in bf16.
+struct MxLayout {
+  size_t q = 0, sc = 0, xn = 0, total = 0;
+  int64_t ldq = 0, lds = 0, ldn = 0;
+};
+MxLayout mx_layout(int64_t rows, int64_t k, int32_t x_format);
+
+// The multi-slice layer behind lora_linear_sliced(_q, _mx) (the C ABI's types;
+// defined in lora_api.cpp).  mx: a microscaled base in place of W.  self_contained: create no library resource --
 // the plan runs on the caller's stream and no launch is timed.
 lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const void *x,
                                  int64_t ldx, const void *W, int64_t ldw, const lora_qweight_t *qw,
                                  int32_t n_slices, const lora_slice_t *slices,
                                  const int32_t *adapter_ids, void *y, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, int32_t path, uint32_t flags, void *stream,
-                                 bool self_contained);
+                                 bool self_contained, const MxBase *mx = nullptr);
 
 }  // namespace lora

@@ -460,8 +460,92 @@ lora_status_t lora_plan_view(const void *workspace, size_t workspace_bytes, int6
 }  // extern "C"
 
 namespace lora {
+// Microscaled base: host checks of what it takes in place of W.
+static lora_status_t check_mx_layer(const MxBase &mx, int64_t M, int64_t k, int64_t d,
+                                    const void *x, int64_t ldx, const void *y, int64_t ldy) {
+  if (mx.x_format != LORA_MX_FP8 && mx.x_format != LORA_MX_FP4) return LORA_ERR_DTYPE;
+  lora_status_t s = check_gemm_mx(M, k, d, mx.W);
+  if (s != LORA_OK || M == 0) return s;
+  if (x == nullptr || y == nullptr) return LORA_ERR_ARG;
+  if (ldx < k || ldy < d || k > (int64_t(1) << 23)) return LORA_ERR_SHAPE;
+  if (k % 8 || ldx % 8 || !aligned16(x) || (uintptr_t)y % 2 != 0) return LORA_ERR_SHAPE;
+  if (mx.norm == nullptr) return LORA_OK;
+  if ((s = check_norm_in(LORA_DTYPE_BF16, M, k, x, ldx, mx.norm)) != LORA_OK) return s;
+  // y is written after every row has been normed; residual_out may be x or
+  // the residual but not the layer's output
+  const lora_norm_t &n = *mx.norm;
+  if (n.residual_out != nullptr) {
+    const uint8_t *h0 = (const uint8_t *)n.residual_out, *y0 = (const uint8_t *)y;
+    const int64_t hs = ((M - 1) * n.ldro + k) * 2, ys = ((M - 1) * ldy + d) * 2;
+    if (h0 < y0 + ys && y0 < h0 + hs) return LORA_ERR_ARG;
+  }
+  return LORA_OK;
+}
+
+// One chunk's rows from row c0 on: normed (where there is a norm) and
+// quantised into the workspace region `reg`, then multiplied with W.
+static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d, int64_t c0,
+                              const uint8_t *xc, int64_t ldx, uint8_t *yc, int64_t ldy,
+                              uint8_t *reg, const MxLayout &XL, hipStream_t st) {
+  hipError_t e;
+  if (mx.norm) {
+    const lora_norm_t &n = *mx.norm;
+    RmsNormArgs a{};
+    a.dtype = LORA_DTYPE_BF16;
+    a.fmt = mx.x_format;
+    a.M = Mc;
+    a.k = k;
+    a.x = xc;
+    a.ldx = ldx;
+    a.res = n.residual ? (const uint16_t *)n.residual + c0 * n.ldr : nullptr;
+    a.ldr = n.ldr;
+    a.w = n.weight;
+    a.h = n.residual_out ? (uint16_t *)n.residual_out + c0 * n.ldro : nullptr;
+    a.ldh = n.ldro;
+    a.y = reg + XL.xn;
+    a.ldy = XL.ldn;
+    a.q = reg + XL.q;
+    a.ldq = XL.ldq;
+    a.sc = reg + XL.sc;
+    a.lds = XL.lds;
+    a.eps = n.eps;
+    e = launch_rmsnorm(a, st);
+  } else {
+    MxQuantArgs a{};
+    a.dtype = LORA_DTYPE_BF16;
+    a.fmt = mx.x_format;
+    a.M = Mc;
+    a.k = k;
+    a.x = xc;
+    a.ldx = ldx;
+    a.q = reg + XL.q;
+    a.ldq = XL.ldq;
+    a.sc = reg + XL.sc;
+    a.lds = XL.lds;
+    e = launch_mx_quantize(a, st);
+  }
+  if (e != hipSuccess) return e;
+  MxGemmArgs g{};
+  g.xfmt = mx.x_format;
+  g.M = (int32_t)Mc;
+  g.N = (int32_t)d;
+  g.nb = (int32_t)((k + 31) / 32);
+  g.x = reg + XL.q;
+  g.ldx = XL.ldq;
+  g.xs = reg + XL.sc;
+  g.ldxs = XL.lds;
+  g.w = (const uint8_t *)mx.W->q;
+  g.ldw = mx.W->ldq;
+  g.wsc = mx.W->scales;
+  g.ldws = mx.W->lds;
+  g.y = (uint16_t *)yc;
+  g.ldy = ldy;
+  return launch_gemm_mx(g, st);
+}
+
 // The layer over several slices; the base weight is dense (W, ldw) or, with
-// qw != nullptr, quantized (bf16 only).  self_contained: use no library
+// qw != nullptr, quantized, or with mx != nullptr microscaled (both bf16
+// only).  self_contained: use no library
 // resource that may need creating -- the plan runs on the caller's stream
 // (no side stream or fork/join events) and no launch is timed.
 lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const void *x,
@@ -469,14 +553,15 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                                  int32_t n_slices, const lora_slice_t *slices,
                                  const int32_t *adapter_ids, void *y, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, int32_t path, uint32_t flags, void *stream,
-                                 bool self_contained) {
+                                 bool self_contained, const MxBase *mx) {
   int32_t S = 0, R = 0;
   int64_t d_total = 0;
   if (slices == nullptr || n_slices < 1 || n_slices > LORA_MAX_SLICES) return LORA_ERR_ARG;
   lora_status_t s = check_slices(n_slices, slices, M, &S, &R, &d_total);
   if (s != LORA_OK) return s;
-  s = qw ? check_q_gemm_args(M, k, d_total, x, ldx, qw, y, ldy)
-         : check_gemm_args(dtype, M, k, d_total, x, ldx, W, ldw, y, ldy);
+  s = mx   ? check_mx_layer(*mx, M, k, d_total, x, ldx, y, ldy)
+      : qw ? check_q_gemm_args(M, k, d_total, x, ldx, qw, y, ldy)
+           : check_gemm_args(dtype, M, k, d_total, x, ldx, W, ldw, y, ldy);
   if (s != LORA_OK) return s;
   if (path != LORA_PATH_AUTO && path != LORA_PATH_GATHER && path != LORA_PATH_SGMV) return LORA_ERR_ARG;
   if ((flags & ~(LORA_FLAG_REUSE_PLAN | LORA_FLAG_SEPARATE_SHRINK)) != 0) return LORA_ERR_ARG;
@@ -487,7 +572,10 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
   if (((uintptr_t)workspace & 255u) != 0) return LORA_ERR_WORKSPACE;
   if ((flags & LORA_FLAG_REUSE_PLAN) && M > kPlanMaxRows) return LORA_ERR_ARG;
   const int64_t first = std::min<int64_t>(M, kPlanMaxRows);
-  if (workspace_bytes < ws_layout(first, S, R, n_slices).total) return LORA_ERR_WORKSPACE;
+  if (workspace_bytes < ws_layout(first, S, R, n_slices).total +
+                            (mx ? mx_layout(first, k, mx->x_format).total : 0))
+    return LORA_ERR_WORKSPACE;
+  const bool dense = !qw && !mx;  // the base GEMM that can carry plan and shrink
 
   // kernel family: MFMA tiles need bf16 operands and ranks <= 64
   const bool mfma_ok = dtype == LORA_DTYPE_BF16 && R <= kMaxRankMfma;
@@ -538,6 +626,11 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
 
     a.x = xc;
     a.y = yc;
+    const MxLayout XL = mx ? mx_layout(Mc, k, mx->x_format) : MxLayout{};
+    if (mx && mx->norm) {  // the adapters read the normed rows
+      a.x = ws + L.total + XL.xn;
+      a.ldx = XL.ldn;
+    }
     a.L = L;
     // rows per MFMA work item: 64-row segment tiles when asked for (SGMV)
     // or when adapters are expected to hold long runs of rows (prefill);
@@ -573,7 +666,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
     // every rank in at most two passes (the second is a fallback for rank
     // sums past the first pass's capacity).
     int32_t fcap = 0;
-    if (!qw && dtype == LORA_DTYPE_BF16 && use_mfma && !(flags & LORA_FLAG_SEPARATE_SHRINK) &&
+    if (dense && dtype == LORA_DTYPE_BF16 && use_mfma && !(flags & LORA_FLAG_SEPARATE_SHRINK) &&
         (int64_t)n_slices * S <= kFusedMaxEntries && S <= 256) {
       // slots, or pools whose pages hold whole A rows (each row one
       // contiguous run the GEMM's loads can take)
@@ -629,12 +722,12 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
     // Where the base GEMM launch can carry the plan, it does (no plan
     // launch, side stream or events: the fork and join cost ~6.5 us each on
     // the stream at the 70B q+v step)
-    const bool in_gemm = !reuse && !qw &&
+    const bool in_gemm = !reuse && dense &&
                          gemm_runs_plan(dtype, Mc, k, d_total, ldx, ldw, gws, gws_bytes, fcap > 0);
     PlanArgs gplan{};
     if (in_gemm) gplan = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
     bool beside = !self_contained && !in_gemm;
-    if (!reuse && !qw && beside) {
+    if (!reuse && dense && beside) {
       KernelFootprint pf, gf;
       const PlanArgs pa = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
       beside = plan_footprint(pa, &pf) &&
@@ -653,6 +746,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
       if (fork && hipEventRecord(ev_join, ps) != hipSuccess) return LORA_ERR_HIP;
     }
     hipError_t e = maybe_timed(self_contained, LORA_K_GEMM, st, [&] {
+      if (mx) return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL, st);
       if (qw) return launch_gemm_q(make_q_args(qw, Mc, k, d_total, xc, ldx, yc, ldy), st);
       // expired split-K waits are counted in the plan header, where
       // lora_check reads them
