@@ -757,78 +757,115 @@ def lora_linear_sliced_q(x: torch.Tensor, W: QWeight, slices, adapter_ids: torch
 MX_FP8, MX_FP4 = 1, 2
 
 
+# The raw handle of a device's current stream, without making a Stream object
+# for it (2 us of a call's 8).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _on(device: torch.device, stream, fn, what: str, *args) -> None:
     """fn(*args, stream) with `device` current (a stream belongs to its
     device); by default on that device's current stream."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        status = fn(*args, stream.cuda_stream)
+    index = device.index
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            status = fn(*args, stream.cuda_stream)
+        with torch.cuda.device(index):
+            status = fn(*args, handle)
     if status != 0:
         raise LoraError(status, what)
 
 
-def _matrix(t: torch.Tensor, name: str, rows: int, cols: int, dtype, device):
-    """(pointer, leading dimension) of a row-major [rows, cols] tensor of
-    this dtype on this device."""
-    if t.dtype != dtype:
+def _matrix(t: torch.Tensor, name: str, shape, dtype, device):
+    """(pointer, leading dimension) of a row-major tensor of this shape (M,
+    k), dtype and device (a GPU)."""
+    if t.dtype is not dtype:
         raise TypeError("%s must be %s" % (name, dtype))
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError("%s must be [%d, %d]" % (name, rows, cols))
-    if t.device != device or not t.is_cuda:
+    if t.shape != shape:
+        raise ValueError("%s must be [%d, %d]" % (name, *shape))
+    if t.device != device:
         raise ValueError("%s must be a tensor on %s" % (name, device))
-    if cols > 1 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
         raise ValueError("%s must have unit stride along its last dimension" % name)
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+
+
+def _device_matrix(x: torch.Tensor, name: str):
+    """(shape, device) of a 2-D device tensor."""
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("%s must be a 2-D device tensor" % name)
+    return x.shape, x.device
 
 
 class MX:
     """A microscaled matrix [rows, k] (include/lora_mx.h, lora_mx_t): codes
     `q`, uint8 [rows, >= ceil(k / 32) * 32 (MX_FP8) or * 16 (MX_FP4)], and a
-    scale byte per 32 elements, uint8 [rows, >= ceil(k / 32)]."""
+    scale byte per 32 elements, `scales`, uint8 [rows, >= ceil(k / 32)]."""
 
-    __slots__ = ("fmt", "q", "scales", "k", "rows", "_c", "_ref")
+    __slots__ = ("fmt", "k", "rows", "device", "_q", "_scales", "_own", "_c", "_ref")
 
     def __init__(self, fmt: int, q: torch.Tensor, scales: torch.Tensor, k: int):
-        if fmt not in (MX_FP8, MX_FP4):
-            raise ValueError("fmt must be MX_FP8 or MX_FP4")
-        if q.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        nb, width = self._sizes(fmt, k)
+        if q.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
             raise TypeError("q and scales must be uint8")
         if not q.is_cuda or q.device != scales.device:
             raise ValueError("q and scales must be tensors on one device")
-        k = int(k)
-        nb = (k + 31) // 32
-        width = nb * (32 if fmt == MX_FP8 else 16)
         if q.dim() != 2 or scales.dim() != 2 or q.shape[0] != scales.shape[0]:
             raise ValueError("q and scales must be 2-D with one row per row of the matrix")
-        if k < 1 or q.shape[1] < width or scales.shape[1] < nb:
+        rows = q.shape[0]
+        if q.shape[1] < width or scales.shape[1] < nb:
             raise ValueError("k = %d needs %d bytes of codes and %d scales a row" % (k, width, nb))
         if q.stride(1) != 1 or scales.stride(1) != 1 and nb > 1:
             raise ValueError("q and scales must have unit stride along their last dimension")
-        self.fmt, self.q, self.scales, self.k, self.rows = int(fmt), q, scales, k, q.shape[0]
-        c = _CMx()
-        c.format = self.fmt
-        c.q = q.data_ptr()
-        c.scales = scales.data_ptr()
-        # a single row may have any stride
-        c.ldq = q.stride(0) if self.rows > 1 else width
-        c.lds = scales.stride(0) if self.rows > 1 else (nb + 3) // 4 * 4
-        self._c = c
-        self._ref = ctypes.byref(c)
+        # a single row may have any stride; scales are read four at a time
+        ldq = q.stride(0) if rows > 1 else width
+        lds = scales.stride(0) if rows > 1 else (nb + 3) // 4 * 4
+        left = scales.untyped_storage().nbytes() - scales.storage_offset()
+        if rows > 0 and left < (rows - 1) * lds + (nb + 3) // 4 * 4:
+            raise ValueError("the last row of scales must have room for a multiple of 4 bytes")
+        self._q, self._scales, self._own = q, scales, None
+        self._set(fmt, k, rows, q.device, q.data_ptr(), ldq, scales.data_ptr(), lds)
+
+    @staticmethod
+    def _sizes(fmt: int, k: int):
+        """(scales, bytes of codes) a row."""
+        if fmt != MX_FP8 and fmt != MX_FP4:
+            raise ValueError("fmt must be MX_FP8 or MX_FP4")
+        if k < 1:
+            raise ValueError("k must be at least 1")
+        nb = (k + 31) // 32
+        return nb, nb * (32 if fmt == MX_FP8 else 16)
+
+    def _set(self, fmt, k, rows, device, q, ldq, scales, lds):
+        self.fmt, self.k, self.rows, self.device = int(fmt), int(k), rows, device
+        self._c = _CMx(self.fmt, q, ldq, scales, lds)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, rows: int, k: int, fmt: int, device="cuda") -> "MX":
         """Uninitialised storage with the least strides the library takes."""
-        nb = (int(k) + 31) // 32
-        q = torch.empty((rows, nb * (32 if fmt == MX_FP8 else 16)), dtype=torch.uint8, device=device)
-        return cls(fmt, q, torch.empty((rows, (nb + 3) // 4 * 4), dtype=torch.uint8, device=device), k)
+        nb, ldq = cls._sizes(fmt, k)
+        lds = (nb + 3) // 4 * 4
+        m = cls.__new__(cls)
+        m._q = m._scales = None  # views of the one buffer, made when asked for
+        m._own = buf = torch.empty(rows * (ldq + lds), dtype=torch.uint8, device=device)
+        p = buf.data_ptr()
+        m._set(fmt, k, rows, buf.device, p, ldq, p + rows * ldq, lds)
+        return m
 
     @property
-    def device(self) -> torch.device:
-        return self.q.device
+    def q(self) -> torch.Tensor:
+        if self._q is None:
+            self._q = self._own[:self.rows * self._c.ldq].view(self.rows, self._c.ldq)
+        return self._q
+
+    @property
+    def scales(self) -> torch.Tensor:
+        if self._scales is None:
+            self._scales = self._own[self.rows * self._c.ldq:].view(self.rows, self._c.lds)
+        return self._scales
 
     def ref(self):
         return self._ref
@@ -839,15 +876,14 @@ def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = Non
     """Microscaled x (float32 or bfloat16 [M, k])."""
     lib = load_library()
     dt = _dtype_code(x)
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError("x must be a 2-D device tensor")
-    M, k = x.shape
+    shape, device = _device_matrix(x, "x")
+    M, k = shape
     if out is None:
-        out = MX.empty(M, k, fmt, x.device)
-    elif out.fmt != fmt or out.rows != M or out.k != k or out.device != x.device:
+        out = MX.empty(M, k, fmt, device)
+    elif out.fmt != fmt or out.rows != M or out.k != k or out.device != device:
         raise ValueError("out must be a [%d, %d] matrix of this format on x's device" % (M, k))
-    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
-    _on(x.device, stream, lib.lora_mx_quantize, "lora_mx_quantize", dt, M, k, xp, ldx, out._ref)
+    xp, ldx = _matrix(x, "x", shape, x.dtype, device)
+    _on(device, stream, lib.lora_mx_quantize, "lora_mx_quantize", dt, M, k, xp, ldx, out._ref)
     return out
 
 
@@ -855,13 +891,14 @@ def lora_mx_dequantize(q: MX, dtype: torch.dtype = torch.bfloat16,
                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values q stands for (float32 or bfloat16 [rows, k])."""
     lib = load_library()
-    if dtype not in _DTYPES:
+    dt = _DTYPES.get(dtype)
+    if dt is None:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    shape = (q.rows, q.k)
     if out is None:
-        out = torch.empty((q.rows, q.k), dtype=dtype, device=q.device)
-    yp, ldy = _matrix(out, "out", q.rows, q.k, dtype, q.device)
-    _on(q.device, stream, lib.lora_mx_dequantize, "lora_mx_dequantize", _DTYPES[dtype], q.rows, q.k,
-        q._ref, yp, ldy)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+    yp, ldy = _matrix(out, "out", shape, dtype, q.device)
+    _on(q.device, stream, lib.lora_mx_dequantize, "lora_mx_dequantize", dt, q.rows, q.k, q._ref, yp, ldy)
     return out
 
 
@@ -870,26 +907,25 @@ class Norm:
     the residual that is added first and the tensor that receives the sum
     (both [M, k]; the sum may go in place of x or of the residual)."""
 
+    __slots__ = ("weight", "eps", "residual", "residual_out")
+
     def __init__(self, weight: torch.Tensor, eps: float = 1e-5,
                  residual: Optional[torch.Tensor] = None,
                  residual_out: Optional[torch.Tensor] = None):
         self.weight, self.eps = weight, float(eps)
         self.residual, self.residual_out = residual, residual_out
 
-    def c(self, x: torch.Tensor) -> _CNorm:
-        M, k = x.shape
+    def c(self, shape, dtype, device) -> _CNorm:
         w = self.weight
-        if w.dtype != x.dtype:
+        if w.dtype is not dtype:
             raise TypeError("the norm's weight must have x's dtype")
-        if w.dim() != 1 or w.shape[0] != k or w.device != x.device or not w.is_contiguous():
-            raise ValueError("the norm's weight must be a contiguous [%d] tensor on x's device" % k)
-        c = _CNorm()
-        c.weight = w.data_ptr()
-        c.eps = self.eps
+        if w.shape != shape[1:] or w.device != device or not w.is_contiguous():
+            raise ValueError("the norm's weight must be a contiguous [%d] tensor on x's device" % shape[1])
+        c = _CNorm(w.data_ptr(), self.eps)
         if self.residual is not None:
-            c.residual, c.ldr = _matrix(self.residual, "residual", M, k, x.dtype, x.device)
+            c.residual, c.ldr = _matrix(self.residual, "residual", shape, dtype, device)
         if self.residual_out is not None:
-            c.residual_out, c.ldro = _matrix(self.residual_out, "residual_out", M, k, x.dtype, x.device)
+            c.residual_out, c.ldro = _matrix(self.residual_out, "residual_out", shape, dtype, device)
         return c
 
 
@@ -899,30 +935,31 @@ def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
     the normed rows microscaled.  y is made if neither is given."""
     lib = load_library()
     dt = _dtype_code(x)
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError("x must be a 2-D device tensor")
-    M, k = x.shape
+    shape, device = _device_matrix(x, "x")
+    dtype = x.dtype
+    M, k = shape
     if y is None and yq is None:
-        y = torch.empty_like(x, memory_format=torch.contiguous_format)
-    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
-    yp, ldy = (None, 0) if y is None else _matrix(y, "y", M, k, x.dtype, x.device)
-    if yq is not None and (yq.rows != M or yq.k != k or yq.device != x.device):
+        y = torch.empty(shape, dtype=dtype, device=device)
+    xp, ldx = _matrix(x, "x", shape, dtype, device)
+    yp, ldy = (None, 0) if y is None else _matrix(y, "y", shape, dtype, device)
+    if yq is not None and (yq.rows != M or yq.k != k or yq.device != device):
         raise ValueError("yq must be a [%d, %d] matrix on x's device" % (M, k))
-    _on(x.device, stream, lib.lora_rmsnorm, "lora_rmsnorm", dt, M, k, xp, ldx,
-        ctypes.byref(norm.c(x)), yp, ldy, None if yq is None else yq._ref)
+    _on(device, stream, lib.lora_rmsnorm, "lora_rmsnorm", dt, M, k, xp, ldx,
+        ctypes.byref(norm.c(shape, dtype, device)), yp, ldy, None if yq is None else yq._ref)
     return y
 
 
 def lora_gemm_mx(x: MX, W: MX, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T on microscaled operands (bfloat16 y [rows of x, rows of W])."""
     lib = load_library()
-    if x.k != W.k or x.device != W.device:
+    device = x.device
+    if x.k != W.k or W.device != device:
         raise ValueError("x and W differ in k or device")
+    shape = (x.rows, W.rows)
     if y is None:
-        y = torch.empty((x.rows, W.rows), dtype=torch.bfloat16, device=x.device)
-    yp, ldy = _matrix(y, "y", x.rows, W.rows, torch.bfloat16, x.device)
-    _on(x.device, stream, lib.lora_gemm_mx, "lora_gemm_mx", x.rows, x.k, W.rows, x._ref, W._ref, yp,
-        ldy)
+        y = torch.empty(shape, dtype=torch.bfloat16, device=device)
+    yp, ldy = _matrix(y, "y", shape, torch.bfloat16, device)
+    _on(device, stream, lib.lora_gemm_mx, "lora_gemm_mx", x.rows, x.k, W.rows, x._ref, W._ref, yp, ldy)
     return y
 
 
@@ -943,32 +980,32 @@ def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Ten
     """lora_linear_sliced over a microscaled stacked base weight: the rows of
     x (normed first with a norm) meet W in x_format, the adapters in bf16."""
     lib = load_library()
-    if x.dtype != torch.bfloat16:
+    dtype = torch.bfloat16
+    if x.dtype is not dtype:
         raise TypeError("x must be bfloat16")
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError("x must be a 2-D device tensor")
-    M, k = x.shape
+    shape, device = _device_matrix(x, "x")
+    M, k = shape
     d_total = sum(sl.d for sl in slices)
-    if W.rows != d_total or W.k != k or W.device != x.device:
+    if W.rows != d_total or W.k != k or W.device != device:
         raise ValueError("W must stack the slices' weights on x's device: [%d, %d] expected" % (d_total, k))
     if y is None:
-        y = torch.empty((M, d_total), dtype=x.dtype, device=x.device)
+        y = torch.empty((M, d_total), dtype=dtype, device=device)
     if workspace is None:
         workspace = torch.zeros(workspace_bytes_sliced_mx(M, k, x_format, slices), dtype=torch.uint8,
-                                device=x.device)
-    xp, ldx = _matrix(x, "x", M, k, x.dtype, x.device)
-    yp, ldy = _matrix(y, "y", M, d_total, x.dtype, x.device)
+                                device=device)
+    xp, ldx = _matrix(x, "x", shape, dtype, device)
+    yp, ldy = _matrix(y, "y", (M, d_total), dtype, device)
     if adapter_ids.numel() != M:
         raise ValueError("adapter_ids must have one entry per row")
     for sl in slices:
         ad = sl.adapters
-        if ad.kind == KIND_SLOTS and ad.A.dtype != x.dtype:
+        if ad.kind == KIND_SLOTS and ad.A.dtype is not dtype:
             raise TypeError("adapter slots must have x's dtype")
         if ad.kind == KIND_SLOTS and (ad.A.shape[2] != k or ad.B.shape[1] != sl.d):
             raise ValueError("adapter slots must be A [S, R, %d] and B [S, %d, R]" % (k, sl.d))
-    _on(x.device, stream, lib.lora_linear_sliced_mx, "lora_linear_sliced_mx", M, k, xp, ldx,
-        None if norm is None else ctypes.byref(norm.c(x)), int(x_format), W._ref, len(slices),
-        _slice_array(slices), _dev(adapter_ids, "adapter_ids", torch.int32), yp, ldy,
+    _on(device, stream, lib.lora_linear_sliced_mx, "lora_linear_sliced_mx", M, k, xp, ldx,
+        None if norm is None else ctypes.byref(norm.c(shape, dtype, device)), int(x_format), W._ref,
+        len(slices), _slice_array(slices), _dev(adapter_ids, "adapter_ids", torch.int32), yp, ldy,
         _dev(workspace, "workspace"), workspace.numel(), int(path), int(flags))
     return y
 
