@@ -364,10 +364,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_gemm_mx_tile(MxGemmArgs p
 }
 
 // ---------------------------------------------------------------------------
-// Large tiles: every load a run of 128 bytes
-// of a row.  What a load into LDS costs is its number of 128-byte lines (2.2
-// cycles of a CU each, measured; half a line costs as much), and that bounds
-// a CU's feed: hence W's pairs of steps also where x goes by steps.
+// Large tiles: every load a run of 128 bytes of a row.  What a load into LDS
+// costs is its number of 128-byte lines (2.2 cycles of a CU each, measured;
+// half a line costs as much), and that bounds a CU's feed: hence W's pairs of
+// steps also where x goes by steps.
 // ---------------------------------------------------------------------------
 
 // k runs in pairs of steps (256 elements).  W's ring holds two pairs, x's STX

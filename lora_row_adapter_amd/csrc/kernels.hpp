@@ -188,7 +188,9 @@ struct MxQuantArgs {
   uint8_t *sc;
   int64_t lds;
 };
-hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t st);
+// plan: run it in this launch, in a workgroup beside the rows' (bf16 rows,
+// only where mx_runs_plan says so).
+hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t st, const PlanArgs *plan = nullptr);
 hipError_t launch_mx_dequantize(const MxQuantArgs &a, hipStream_t st);
 struct RmsNormArgs {
   int32_t dtype;
@@ -201,7 +203,8 @@ struct RmsNormArgs {
   int64_t ldq, lds;
   float eps;
 };
-hipError_t launch_rmsnorm(const RmsNormArgs &a, hipStream_t st);
+hipError_t launch_rmsnorm(const RmsNormArgs &a, hipStream_t st, const PlanArgs *plan = nullptr);
+bool mx_runs_plan(int64_t M, int64_t k, int32_t n_adapters, bool norm);
 // y = x W^T: x fp8 or fp4, W fp4, y bf16.
 struct MxGemmArgs {
   int32_t xfmt;  // lora_mxformat_t of x

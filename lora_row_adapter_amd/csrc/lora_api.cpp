@@ -483,10 +483,11 @@ static lora_status_t check_mx_layer(const MxBase &mx, int64_t M, int64_t k, int6
 }
 
 // One chunk's rows from row c0 on: normed (where there is a norm) and
-// quantised into the workspace region `reg`, then multiplied with W.
+// quantised into the workspace region `reg`, with the plan beside where one
+// is given, then multiplied with W.
 static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d, int64_t c0,
                               const uint8_t *xc, int64_t ldx, uint8_t *yc, int64_t ldy,
-                              uint8_t *reg, const MxLayout &XL, hipStream_t st) {
+                              uint8_t *reg, const MxLayout &XL, const PlanArgs *plan, hipStream_t st) {
   hipError_t e;
   if (mx.norm) {
     const lora_norm_t &n = *mx.norm;
@@ -509,7 +510,7 @@ static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d
     a.sc = reg + XL.sc;
     a.lds = XL.lds;
     a.eps = n.eps;
-    e = launch_rmsnorm(a, st);
+    e = launch_rmsnorm(a, st, plan);
   } else {
     MxQuantArgs a{};
     a.dtype = LORA_DTYPE_BF16;
@@ -522,7 +523,7 @@ static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d
     a.ldq = XL.ldq;
     a.sc = reg + XL.sc;
     a.lds = XL.lds;
-    e = launch_mx_quantize(a, st);
+    e = launch_mx_quantize(a, st, plan);
   }
   if (e != hipSuccess) return e;
   MxGemmArgs g{};
@@ -724,9 +725,11 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
     // the stream at the 70B q+v step)
     const bool in_gemm = !reuse && dense &&
                          gemm_runs_plan(dtype, Mc, k, d_total, ldx, ldw, gws, gws_bytes, fcap > 0);
+    // and so does a microscaled layer's first launch, the norm or quantising
+    const bool in_prep = !reuse && mx && mx_runs_plan(Mc, k, S, mx->norm != nullptr);
     PlanArgs gplan{};
-    if (in_gemm) gplan = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
-    bool beside = !self_contained && !in_gemm;
+    if (in_gemm || in_prep) gplan = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
+    bool beside = !self_contained && !in_gemm && !in_prep;
     if (!reuse && dense && beside) {
       KernelFootprint pf, gf;
       const PlanArgs pa = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
@@ -735,7 +738,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                fits_beside(gf, pf);
     }
     const bool fork = !reuse && beside && !self_contained && side::get(&ps, &ev_fork, &ev_join);
-    if (!reuse && !in_gemm) {
+    if (!reuse && !in_gemm && !in_prep) {
       if (fork) {
         if (hipEventRecord(ev_fork, st) != hipSuccess || hipStreamWaitEvent(ps, ev_fork, 0) != hipSuccess)
           return LORA_ERR_HIP;
@@ -746,7 +749,9 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
       if (fork && hipEventRecord(ev_join, ps) != hipSuccess) return LORA_ERR_HIP;
     }
     hipError_t e = maybe_timed(self_contained, LORA_K_GEMM, st, [&] {
-      if (mx) return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL, st);
+      if (mx)
+        return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL,
+                           in_prep ? &gplan : nullptr, st);
       if (qw) return launch_gemm_q(make_q_args(qw, Mc, k, d_total, xc, ldx, yc, ldy), st);
       // expired split-K waits are counted in the plan header, where
       // lora_check reads them

@@ -2,12 +2,13 @@
 // norm with a microscaled output (include/lora_mx.h).
 //
 // All three are one pass over the data and bound by its bytes.  A row is cut
-// into chunks of eight elements, one lane each, so a block of 32 is a quad of
-// lanes: its largest magnitude takes two DPP moves, and a wave's loads and
-// stores are contiguous runs of 16 bytes a lane.
+// into chunks of 16 bytes, one lane each, so a block of 32 elements is four
+// (bf16) or eight (fp32) lanes: its largest magnitude takes two or three DPP
+// moves, and a wave's loads and stores of values are contiguous.
 #include <algorithm>
 
 #include "mx_device.hpp"
+#include "plan_body.hpp"
 
 namespace lora {
 
@@ -17,94 +18,97 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// A workgroup covers `ty` rows x `tx` chunk columns (tx a power of two, ty *
-// tx = 256) in each of UNR steps along the row; blockIdx.x runs over column
-// segments first.
+// A workgroup covers (its threads >> log_tx) rows x 1 << log_tx chunk columns
+// in each of UNR steps along the row; workgroups run over column segments
+// first.
 struct RowGrid {
   int32_t log_tx;
-  uint32_t nseg;    // column segments per row group
-  int64_t chunks;   // chunks per row: ceil(k / 32) * 4
+  uint32_t nseg;   // column segments per row group
+  int64_t chunks;  // chunks per row, whole blocks
 };
 
-template <typename T, int FMT, int UNR>
-__global__ __launch_bounds__(kThreads) void k_mx_quantize(const T *x, int64_t ldx, int64_t M,
-                                                          int64_t k, RowGrid g, uint8_t *q,
-                                                          int64_t ldq, uint8_t *sc, int64_t lds) {
-  const int tx = 1 << g.log_tx;
-  const int lx = threadIdx.x & (tx - 1);
-  const uint32_t grp = blockIdx.x / g.nseg, seg = blockIdx.x - grp * g.nseg;
-  const int64_t m = (int64_t)grp * (kThreads >> g.log_tx) + (threadIdx.x >> g.log_tx);
-  if (m >= M) return;  // whole quads leave: tx >= 4
+struct Rows {  // a dense matrix and its microscaled form
+  void *x;
+  int64_t ldx;
+  uint8_t *q, *sc;
+  int64_t ldq, lds;
+  int64_t M, k;
+};
+
+template <typename T, int FMT, int UNR, int NT>
+__device__ __forceinline__ void quantize_rows(const Rows &a, const RowGrid &g, uint32_t block) {
+  using C = Chunk<T>;
+  const int lx = threadIdx.x & ((1 << g.log_tx) - 1);
+  const uint32_t grp = block / g.nseg, seg = block - grp * g.nseg;
+  const int64_t m = (int64_t)grp * (NT >> g.log_tx) + (threadIdx.x >> g.log_tx);
+  if (m >= a.M) return;  // whole blocks leave: a row has at least a block's lanes
   const int64_t c0 = (int64_t)seg * (UNR << g.log_tx) + lx;
-  const T *row = x + m * ldx;
-  Chunk<T> v[UNR];
+  const T *row = (const T *)a.x + m * a.ldx;
+  C v[UNR];
 #pragma unroll
   for (int i = 0; i < UNR; ++i) {
     const int64_t c = c0 + ((int64_t)i << g.log_tx);
-    load_chunk(v[i], row, c, chunk_len(c, k));
+    v[i].load(row, c, C::len(c, a.k));
   }
 #pragma unroll
   for (int i = 0; i < UNR; ++i) {
     const int64_t c = c0 + ((int64_t)i << g.log_tx);
-    float f[8];
+    float f[C::kElems];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = v[i].get(e);
-    quantise_chunk<FMT>(f, c, c < g.chunks, q + m * ldq, sc + m * lds);
+    for (int e = 0; e < C::kElems; ++e) f[e] = v[i].get(e);
+    quantise_chunk<FMT>(f, c, c < g.chunks, a.q + m * a.ldq, a.sc + m * a.lds);
   }
 }
 
 template <typename T, int FMT, int UNR>
-__global__ __launch_bounds__(kThreads) void k_mx_dequantize(const uint8_t *q, int64_t ldq,
-                                                            const uint8_t *sc, int64_t lds,
-                                                            int64_t M, int64_t k, RowGrid g, T *y,
-                                                            int64_t ldy) {
-  const int tx = 1 << g.log_tx;
-  const int lx = threadIdx.x & (tx - 1);
+__global__ __launch_bounds__(kThreads) void k_mx_quantize(Rows a, RowGrid g) {
+  quantize_rows<T, FMT, UNR, kThreads>(a, g, blockIdx.x);
+}
+
+template <typename T, int FMT, int UNR>
+__global__ __launch_bounds__(kThreads) void k_mx_dequantize(Rows a, RowGrid g) {
+  using C = Chunk<T>;
+  constexpr int N = C::kElems;
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  const int lx = threadIdx.x & ((1 << g.log_tx) - 1);
   const uint32_t grp = blockIdx.x / g.nseg, seg = blockIdx.x - grp * g.nseg;
   const int64_t m = (int64_t)grp * (kThreads >> g.log_tx) + (threadIdx.x >> g.log_tx);
-  if (m >= M) return;
+  if (m >= a.M) return;
   const int64_t c0 = (int64_t)seg * (UNR << g.log_tx) + lx;
-  const uint8_t *qrow = q + m * ldq, *srow = sc + m * lds;
-  uint2 w[UNR];
-  uint32_t s[UNR];
+  const uint8_t *qrow = a.q + m * a.ldq, *srow = a.sc + m * a.lds;
+  uint32_t w[UNR][2], s[UNR];  // N codes of fp8 or fp4
 #pragma unroll
   for (int i = 0; i < UNR; ++i) {
     const int64_t c = c0 + ((int64_t)i << g.log_tx);
-    const bool live = c < g.chunks;
-    w[i] = make_uint2(0, 0);
-    s[i] = 0;
-    if (live) {
-      if constexpr (FMT == kFp8) w[i] = *reinterpret_cast<const uint2 *>(qrow + c * 8);
-      else w[i].x = *reinterpret_cast<const uint32_t *>(qrow + c * 4);
-      s[i] = srow[c >> 2];
+    w[i][0] = w[i][1] = s[i] = 0;
+    if (c < g.chunks) {
+      if constexpr (FMT == kFp8) __builtin_memcpy(w[i], __builtin_assume_aligned(qrow + c * N, N), N);
+      else __builtin_memcpy(w[i], __builtin_assume_aligned(qrow + c * (N / 2), N / 2), N / 2);
+      s[i] = srow[c / C::kLanes];
     }
   }
 #pragma unroll
   for (int i = 0; i < UNR; ++i) {
     const int64_t c = c0 + ((int64_t)i << g.log_tx);
     const float f = scale_value(s[i]);
-    Chunk<T> o;
-    typedef float f32x2_t __attribute__((ext_vector_type(2)));
-    if constexpr (FMT == kFp8) {
-      const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i].x, false);
-      const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i].x, true);
-      const f32x2_t d = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i].y, false);
-      const f32x2_t e = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i].y, true);
-      o.set2(0, a[0] * f, a[1] * f);
-      o.set2(2, b[0] * f, b[1] * f);
-      o.set2(4, d[0] * f, d[1] * f);
-      o.set2(6, e[0] * f, e[1] * f);
-    } else {
-      const f32x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i].x, 1.0f, 0);
-      const f32x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i].x, 1.0f, 1);
-      const f32x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i].x, 1.0f, 2);
-      const f32x2_t e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i].x, 1.0f, 3);
-      o.set2(0, a[0] * f, a[1] * f);
-      o.set2(2, b[0] * f, b[1] * f);
-      o.set2(4, d[0] * f, d[1] * f);
-      o.set2(6, e[0] * f, e[1] * f);
+    C o;
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      f32x2_t lo, hi;
+      if constexpr (FMT == kFp8) {
+        lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i][e / 4], false);
+        hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i][e / 4], true);
+      } else if (e == 0) {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], 1.0f, 0);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], 1.0f, 1);
+      } else {
+        lo = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], 1.0f, 2);
+        hi = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[i][0], 1.0f, 3);
+      }
+      o.set2(e, lo[0] * f, lo[1] * f);
+      o.set2(e + 2, hi[0] * f, hi[1] * f);
     }
-    store_chunk(o, y + m * ldy, c, chunk_len(c, k));
+    o.store((T *)a.x + m * a.ldx, c, C::len(c, a.k));
   }
 }
 
@@ -133,125 +137,156 @@ struct NormArgs {
   int64_t ldx, ldr, ldh, ldy, ldq, lds;
   int64_t M, k, chunks;
   double eps, inv_k;
-  int32_t log_tpr;  // threads per row (a power of two, 4 .. 1024)
+  int32_t log_tpr;  // threads per row (a power of two, at most the workgroup's)
 };
 
-// Sum over the threads of a row (1 << log_tpr of them, aligned).
+// Sum over the threads of a row, which are 1 << log_tpr neighbours; rows of
+// several waves put their waves' sums in `red`.
 __device__ __forceinline__ double row_sum(double s, int log_tpr, double *red) {
   const int in_wave = log_tpr < 6 ? log_tpr : 6;
   for (int i = 0; i < in_wave; ++i) s += __shfl_xor(s, 1 << i, 64);
-  if (log_tpr > 6) {  // one row per workgroup
-    const int nw = 1 << (log_tpr - 6);
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+  if (log_tpr > 6) {
+    const int nw = 1 << (log_tpr - 6), wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = s;
     __syncthreads();
     s = 0;
-    for (int i = 0; i < nw; ++i) s += red[i];
+    for (int i = 0; i < nw; ++i) s += red[(wave & ~(nw - 1)) + i];
   }
   return s;
 }
 
-// One row per 1 << log_tpr threads.  C > 0: each thread keeps its C chunks of
-// x and the residual in registers, so every input is read once; C == 0: rows
-// too long for that are read twice.
-template <typename T, int FMT, int C>
-__global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
-  __shared__ double red[16];
+// The rows of workgroup `block`, one per 1 << log_tpr threads.  NC > 0: each
+// thread keeps its NC chunks of x and the residual in registers, so every
+// input is read once; NC == 0: rows too long for that are read twice.
+template <typename T, int FMT, int NC>
+__device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, double *red) {
+  using C = Chunk<T>;
+  constexpr int N = C::kElems;
   const int tpr = 1 << a.log_tpr;
   const int lx = threadIdx.x & (tpr - 1);
-  const int64_t m = (int64_t)blockIdx.x * (blockDim.x >> a.log_tpr) + (threadIdx.x >> a.log_tpr);
-  if (m >= a.M) return;  // whole rows leave; rows of several waves are alone in their workgroup
+  const int64_t at = (int64_t)block * (blockDim.x >> a.log_tpr) + (threadIdx.x >> a.log_tpr);
+  // rows past the last redo it and write nothing: every thread meets the barrier
+  const bool live = at < a.M;
+  const int64_t m = live ? at : a.M - 1;
   const T *x = (const T *)a.x + m * a.ldx;
   const T *r = a.res ? (const T *)a.res + m * a.ldr : nullptr;
   const T *w = (const T *)a.w;
   T *h = a.h ? (T *)a.h + m * a.ldh : nullptr;
   T *y = a.y ? (T *)a.y + m * a.ldy : nullptr;
-  uint8_t *q = FMT ? a.q + m * a.ldq : nullptr;
-  uint8_t *sc = FMT ? a.sc + m * a.lds : nullptr;
 
-  auto finish = [&](const Chunk<T> &xv, const Chunk<T> &rv, int64_t c, int n, double rstd) {
-    Chunk<T> wv, o;
-    load_chunk(wv, w, c, n);
-    float f[8];
-    double hv[8];
+  auto load = [&](int64_t c, int n, C &xv, C &rv) {
+    xv.load(x, c, n);
+    if (r) rv.load(r, c, n);
+    else rv.zero();
+  };
+  auto squares = [&](const C &xv, const C &rv, double s) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) hv[e] = (double)xv.get(e) + (double)rv.get(e);
+    for (int e = 0; e < N; ++e) {
+      const double v = (double)xv.get(e) + (double)rv.get(e);
+      s = fma(v, v, s);
+    }
+    return s;
+  };
+  auto finish = [&](const C &xv, const C &rv, const C &wv, int64_t c, int n, double rstd) {
+    C o;
+    float f[N];
+    double hv[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) hv[e] = (double)xv.get(e) + (double)rv.get(e);
     if (h != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) o.set2(e, to_out<T>(hv[e]), to_out<T>(hv[e + 1]));
-      store_chunk(o, h, c, n);
+      for (int e = 0; e < N; e += 2) o.set2(e, to_out<T>(hv[e]), to_out<T>(hv[e + 1]));
+      o.store(h, c, n);
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) hv[e] = hv[e] * rstd * (double)wv.get(e);
+    for (int e = 0; e < N; ++e) hv[e] = hv[e] * rstd * (double)wv.get(e);
     if (sizeof(T) == 4 && y != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) o.set2(e, (float)hv[e], (float)hv[e + 1]);
-      store_chunk(o, y, c, n);
+      for (int e = 0; e < N; e += 2) o.set2(e, (float)hv[e], (float)hv[e + 1]);
+      o.store(y, c, n);
     }
     if (FMT || sizeof(T) == 2) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = to_odd(hv[e]);
+      for (int e = 0; e < N; ++e) f[e] = to_odd(hv[e]);
     }
     if (sizeof(T) == 2 && y != nullptr) {
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) o.set2(e, f[e], f[e + 1]);
-      store_chunk(o, y, c, n);
+      for (int e = 0; e < N; e += 2) o.set2(e, f[e], f[e + 1]);
+      o.store(y, c, n);
     }
     if constexpr (FMT != 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = e < n ? f[e] : 0.f;  // 0 * inf past the row's end
-      quantise_chunk<FMT>(f, c, c < a.chunks, q, sc);
+      for (int e = 0; e < N; ++e) f[e] = e < n ? f[e] : 0.f;  // 0 * inf past the row's end
+      quantise_chunk<FMT>(f, c, true, a.q + m * a.ldq, a.sc + m * a.lds);
     }
   };
 
   double s = 0;
-  if constexpr (C > 0) {
-    Chunk<T> xv[C], rv[C];
+  if constexpr (NC > 0) {
+    C xv[NC], rv[NC], wv[NC];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+    for (int i = 0; i < NC; ++i) {
       const int64_t c = ((int64_t)i << a.log_tpr) + lx;
-      const int n = chunk_len(c, a.k);
-      load_chunk(xv[i], x, c, n);
-      if (r) load_chunk(rv[i], r, c, n);
-      else rv[i].zero();
+      load(c, C::len(c, a.k), xv[i], rv[i]);
+    }
+    // the weight too, ahead of the sum: one row's time is its loads' latency
+#pragma unroll
+    for (int i = 0; i < NC; ++i) {
+      const int64_t c = ((int64_t)i << a.log_tpr) + lx;
+      wv[i].load(w, c, C::len(c, a.k));
     }
 #pragma unroll
-    for (int i = 0; i < C; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double v = (double)xv[i].get(e) + (double)rv[i].get(e);
-        s = fma(v, v, s);
-      }
+    for (int i = 0; i < NC; ++i) s = squares(xv[i], rv[i], s);
     s = row_sum(s, a.log_tpr, red);
+    if (!live) return;
     const double rstd = 1.0 / sqrt(s * a.inv_k + a.eps);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
+    for (int i = 0; i < NC; ++i) {
       const int64_t c = ((int64_t)i << a.log_tpr) + lx;
-      if (c < a.chunks) finish(xv[i], rv[i], c, chunk_len(c, a.k), rstd);
+      if (c < a.chunks) finish(xv[i], rv[i], wv[i], c, C::len(c, a.k), rstd);
     }
   } else {
+    C xv, rv;
     for (int64_t c = lx; c < a.chunks; c += tpr) {
-      Chunk<T> xv, rv;
-      const int n = chunk_len(c, a.k);
-      load_chunk(xv, x, c, n);
-      if (r) load_chunk(rv, r, c, n);
-      else rv.zero();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double v = (double)xv.get(e) + (double)rv.get(e);
-        s = fma(v, v, s);
-      }
+      load(c, C::len(c, a.k), xv, rv);
+      s = squares(xv, rv, s);
     }
     s = row_sum(s, a.log_tpr, red);
+    if (!live) return;
     const double rstd = 1.0 / sqrt(s * a.inv_k + a.eps);
     for (int64_t c = lx; c < a.chunks; c += tpr) {
-      Chunk<T> xv, rv;
-      const int n = chunk_len(c, a.k);
-      load_chunk(xv, x, c, n);
-      if (r) load_chunk(rv, r, c, n);
-      else rv.zero();
-      finish(xv, rv, c, n, rstd);
+      const int n = C::len(c, a.k);
+      load(c, n, xv, rv);
+      C wv;
+      wv.load(w, c, n);
+      finish(xv, rv, wv, c, n, rstd);
     }
   }
+}
+
+template <typename T, int FMT, int NC>
+__global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
+  __shared__ double red[16];
+  rmsnorm_rows<T, FMT, NC>(a, blockIdx.x, red);
+}
+
+// The layer's plan beside the rows' work: workgroup 0 runs it, the others the
+// rows.  It needs the ids alone, so it hides behind the norm (or the
+// quantising) without a stream of its own, whose fork and join cost 6 us:
+// a layer of 512 rows, 8192 -> 9216, goes from 95 to 87 us, one of 8192 rows,
+// 4096 -> 4096, from 158 to 151.
+template <int FMT, int NT>
+__global__ __launch_bounds__(NT) void k_rmsnorm_plan(NormArgs a, PlanArgs plan, uint32_t lds_bytes) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t plan_lds[];
+  __shared__ double red[16];
+  if (blockIdx.x == 0) plan_detail::plan_body<NT>(plan, plan_lds, lds_bytes);
+  else rmsnorm_rows<uint16_t, FMT, 2>(a, blockIdx.x - 1, red);
+}
+template <int FMT, int NT>
+__global__ __launch_bounds__(NT) void k_mx_quantize_plan(Rows a, RowGrid g, PlanArgs plan, uint32_t lds_bytes) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t plan_lds[];
+  if (blockIdx.x == 0) plan_detail::plan_body<NT>(plan, plan_lds, lds_bytes);
+  else quantize_rows<uint16_t, FMT, 4, NT>(a, g, blockIdx.x - 1);
 }
 
 int log2_up(int64_t v, int lo, int hi) {
@@ -264,19 +299,34 @@ int log2_up(int64_t v, int lo, int hi) {
 // taller matrices take several launches over slabs of rows.
 constexpr int64_t kMaxBlocks = int64_t(1) << 21;
 
-// Rows of at least 4 chunks; segments of up to 256 x UNR chunks.  Calls
-// launch(first row, rows, workgroups) for each slab.
-template <typename F>
-hipError_t over_slabs(int64_t M, int64_t k, int unr, RowGrid *g, F &&launch) {
-  g->chunks = (k + kBlock - 1) / kBlock * 4;
-  g->log_tx = log2_up((g->chunks + unr - 1) / unr, 2, 8);
-  const int64_t per = (int64_t)unr << g->log_tx;
-  g->nseg = (uint32_t)((g->chunks + per - 1) / per);
-  const int64_t rows = kThreads >> g->log_tx;
-  const int64_t slab = rows * std::max<int64_t>(1, kMaxBlocks / g->nseg);
-  for (int64_t m0 = 0; m0 < M; m0 += slab) {
-    const int64_t n = std::min(slab, M - m0);
-    launch(m0, n, (unsigned)((n + rows - 1) / rows * g->nseg));
+// Grid of k_mx_quantize / k_mx_dequantize, UNR steps a thread.
+template <typename T>
+RowGrid row_grid(int64_t k, int unr) {
+  RowGrid g;
+  constexpr int lanes = Chunk<T>::kLanes;
+  g.chunks = (k + kBlock - 1) / kBlock * lanes;
+  g.log_tx = log2_up((g.chunks + unr - 1) / unr, lanes == 4 ? 2 : 3, 8);
+  const int64_t per = (int64_t)unr << g.log_tx;
+  g.nseg = (uint32_t)((g.chunks + per - 1) / per);
+  return g;
+}
+
+Rows rows_of(const MxQuantArgs &a) {
+  return Rows{const_cast<void *>(a.x), a.ldx, a.q, a.sc, a.ldq, a.lds, a.M, a.k};
+}
+
+// launch(rows, workgroups) for each slab of rows.
+template <typename T, typename F>
+hipError_t over_slabs(const MxQuantArgs &a, const RowGrid &g, F &&launch) {
+  const int64_t rows = kThreads >> g.log_tx;
+  const int64_t slab = rows * std::max<int64_t>(1, kMaxBlocks / g.nseg);
+  for (int64_t m0 = 0; m0 < a.M; m0 += slab) {
+    Rows r = rows_of(a);
+    r.M = std::min(slab, a.M - m0);
+    r.x = (T *)r.x + m0 * r.ldx;
+    r.q += m0 * r.ldq;
+    r.sc += m0 * r.lds;
+    launch(r, (unsigned)((r.M + rows - 1) / rows * g.nseg));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -285,40 +335,47 @@ hipError_t over_slabs(int64_t M, int64_t k, int unr, RowGrid *g, F &&launch) {
 
 template <typename T, int FMT>
 hipError_t quantize_t(const MxQuantArgs &a, hipStream_t st) {
-  constexpr int UNR = 4;
-  RowGrid g;
-  return over_slabs(a.M, a.k, UNR, &g, [&](int64_t m0, int64_t n, unsigned blocks) {
-    hipLaunchKernelGGL((k_mx_quantize<T, FMT, UNR>), dim3(blocks), dim3(kThreads), 0, st,
-                       (const T *)a.x + m0 * a.ldx, a.ldx, n, a.k, g, a.q + m0 * a.ldq, a.ldq,
-                       a.sc + m0 * a.lds, a.lds);
+  constexpr int UNR = sizeof(T) == 4 ? 2 : 4;  // 9216 x 8192 fp32: 60 us, with 4 63, 1 69
+  const RowGrid g = row_grid<T>(a.k, UNR);
+  return over_slabs<T>(a, g, [&](const Rows &r, unsigned blocks) {
+    hipLaunchKernelGGL((k_mx_quantize<T, FMT, UNR>), dim3(blocks), dim3(kThreads), 0, st, r, g);
   });
 }
 
 template <typename T, int FMT>
 hipError_t dequantize_t(const MxQuantArgs &a, hipStream_t st) {
   constexpr int UNR = 4;
-  RowGrid g;
-  return over_slabs(a.M, a.k, UNR, &g, [&](int64_t m0, int64_t n, unsigned blocks) {
-    hipLaunchKernelGGL((k_mx_dequantize<T, FMT, UNR>), dim3(blocks), dim3(kThreads), 0, st,
-                       a.q + m0 * a.ldq, a.ldq, a.sc + m0 * a.lds, a.lds, n, a.k, g,
-                       (T *)const_cast<void *>(a.x) + m0 * a.ldx, a.ldx);
+  const RowGrid g = row_grid<T>(a.k, UNR);
+  return over_slabs<T>(a, g, [&](const Rows &r, unsigned blocks) {
+    hipLaunchKernelGGL((k_mx_dequantize<T, FMT, UNR>), dim3(blocks), dim3(kThreads), 0, st, r, g);
   });
+}
+
+// Threads per row and chunks per thread (0: the row is read twice).  Two
+// chunks a thread keep most loads in flight for a workgroup that waits once:
+// 8192 x 8192 bf16 with a residual and fp8 codes takes 124 us, with one chunk
+// 140, four 130, eight 347 (registers); 64 rows 6.0, 6.1, 7.6 and 24 us.
+struct NormShape {
+  int log_tpr, nc, block;
+};
+template <typename T>
+NormShape norm_shape(int64_t chunks) {
+  NormShape s;
+  s.log_tpr = log2_up((chunks + 1) / 2, Chunk<T>::kLanes == 4 ? 2 : 3, 10);
+  const int64_t per = (chunks + (int64_t(1) << s.log_tpr) - 1) >> s.log_tpr;
+  s.nc = per <= 2 ? 2 : per <= 4 ? 4 : 0;
+  s.block = std::max(kThreads, 1 << s.log_tpr);
+  return s;
 }
 
 template <typename T, int FMT>
 hipError_t rmsnorm_t(NormArgs a, hipStream_t st) {
-  constexpr int CMAX = 4;
-  // threads per row: up to four chunks each; rows past 1024 x 4 chunks are
-  // read twice
-  a.log_tpr = log2_up((a.chunks + CMAX - 1) / CMAX, 2, 10);
-  const int64_t per = (a.chunks + (int64_t(1) << a.log_tpr) - 1) >> a.log_tpr;
-  // several rows to a workgroup while a row takes at most a wave
-  const int block = a.log_tpr > 6 ? 1 << a.log_tpr : kThreads;
-  const int64_t rows = block >> a.log_tpr;
-  const int64_t M = a.M;
+  const NormShape sh = norm_shape<T>(a.chunks);
+  a.log_tpr = sh.log_tpr;
+  const int64_t rows = sh.block >> sh.log_tpr;
   const NormArgs all = a;
-  for (int64_t m0 = 0; m0 < M; m0 += rows * kMaxBlocks) {
-    a.M = std::min(rows * kMaxBlocks, M - m0);
+  for (int64_t m0 = 0; m0 < all.M; m0 += rows * kMaxBlocks) {
+    a.M = std::min(rows * kMaxBlocks, all.M - m0);
     a.x = (const T *)all.x + m0 * a.ldx;
     if (all.res) a.res = (const T *)all.res + m0 * a.ldr;
     if (all.h) a.h = (T *)all.h + m0 * a.ldh;
@@ -327,10 +384,9 @@ hipError_t rmsnorm_t(NormArgs a, hipStream_t st) {
       a.q = all.q + m0 * a.ldq;
       a.sc = all.sc + m0 * a.lds;
     }
-    const dim3 grid((unsigned)((a.M + rows - 1) / rows)), blk(block);
-    if (per <= 1) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 1>), grid, blk, 0, st, a);
-    else if (per <= 2) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 2>), grid, blk, 0, st, a);
-    else if (per <= CMAX) hipLaunchKernelGGL((k_rmsnorm<T, FMT, CMAX>), grid, blk, 0, st, a);
+    const dim3 grid((unsigned)((a.M + rows - 1) / rows)), blk(sh.block);
+    if (sh.nc == 2) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 2>), grid, blk, 0, st, a);
+    else if (sh.nc == 4) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 4>), grid, blk, 0, st, a);
     else hipLaunchKernelGGL((k_rmsnorm<T, FMT, 0>), grid, blk, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -338,10 +394,55 @@ hipError_t rmsnorm_t(NormArgs a, hipStream_t st) {
   return hipSuccess;
 }
 
+// The plan beside the rows' work is the one for few adapters, whose LDS (2 to
+// 10 KiB up to 1024 rows, 48 KiB for 8192) every workgroup of the launch is
+// given: past 1024 rows the workgroups are of 1024 threads, of which a CU
+// holds two at most anyway, and the plan is as fast as its own kernel.
+constexpr int kPlanAdapters = 64;
+constexpr int64_t kPlanCols = int64_t(1) << 20;  // one launch, so a grid within 32 bits of threads
+
+template <int FMT, int NT>
+void norm_plan(const NormArgs &a, const PlanArgs &p, hipStream_t st) {
+  const size_t lds = plan_detail::plan_small_lds(p.M, NT);
+  const int64_t rows = NT >> a.log_tpr;
+  hipLaunchKernelGGL((k_rmsnorm_plan<FMT, NT>), dim3((unsigned)((a.M + rows - 1) / rows + 1)), dim3(NT),
+                     lds, st, a, p, (uint32_t)lds);
+}
+template <int FMT>
+void norm_plan(const NormArgs &a, int block, const PlanArgs &p, hipStream_t st) {
+  if (p.M > 1024 || block > 512) norm_plan<FMT, 1024>(a, p, st);
+  else if (block > 256) norm_plan<FMT, 512>(a, p, st);
+  else norm_plan<FMT, 256>(a, p, st);
+}
+
+template <int FMT, int NT>
+void quantize_plan(const MxQuantArgs &a, const PlanArgs &p, hipStream_t st) {
+  const RowGrid g = row_grid<uint16_t>(a.k, 4);
+  const size_t lds = plan_detail::plan_small_lds(p.M, NT);
+  const int64_t rows = NT >> g.log_tx;
+  hipLaunchKernelGGL((k_mx_quantize_plan<FMT, NT>), dim3((unsigned)((a.M + rows - 1) / rows * g.nseg + 1)),
+                     dim3(NT), lds, st, rows_of(a), g, p, (uint32_t)lds);
+}
+template <int FMT>
+void quantize_plan(const MxQuantArgs &a, const PlanArgs &p, hipStream_t st) {
+  if (p.M > 1024) quantize_plan<FMT, 1024>(a, p, st);
+  else quantize_plan<FMT, kThreads>(a, p, st);
+}
 }  // namespace
 
-hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t st) {
+bool mx_runs_plan(int64_t M, int64_t k, int32_t n_adapters, bool norm) {
+  if (M < 1 || M > kPlanMaxRows || k > kPlanCols || n_adapters > kPlanAdapters) return false;
+  return !norm || norm_shape<uint16_t>((k + kBlock - 1) / kBlock * 4).nc == 2;
+}
+
+hipError_t launch_mx_quantize(const MxQuantArgs &a, hipStream_t st, const PlanArgs *plan) {
   if (a.M <= 0) return hipSuccess;
+  if (plan != nullptr) {
+    if (a.dtype != LORA_DTYPE_BF16 || !mx_runs_plan(a.M, a.k, plan->S, false)) return hipErrorInvalidValue;
+    if (a.fmt == kFp8) quantize_plan<kFp8>(a, *plan, st);
+    else quantize_plan<kFp4>(a, *plan, st);
+    return hipGetLastError();
+  }
   if (a.dtype == LORA_DTYPE_BF16)
     return a.fmt == kFp8 ? quantize_t<uint16_t, kFp8>(a, st) : quantize_t<uint16_t, kFp4>(a, st);
   return a.fmt == kFp8 ? quantize_t<float, kFp8>(a, st) : quantize_t<float, kFp4>(a, st);
@@ -354,16 +455,25 @@ hipError_t launch_mx_dequantize(const MxQuantArgs &a, hipStream_t st) {
   return a.fmt == kFp8 ? dequantize_t<float, kFp8>(a, st) : dequantize_t<float, kFp4>(a, st);
 }
 
-hipError_t launch_rmsnorm(const RmsNormArgs &n, hipStream_t st) {
+hipError_t launch_rmsnorm(const RmsNormArgs &n, hipStream_t st, const PlanArgs *plan) {
   if (n.M <= 0) return hipSuccess;
   NormArgs a{};
   a.x = n.x; a.res = n.res; a.w = n.w; a.h = n.h; a.y = n.y;
   a.q = n.q; a.sc = n.sc;
   a.ldx = n.ldx; a.ldr = n.ldr; a.ldh = n.ldh; a.ldy = n.ldy; a.ldq = n.ldq; a.lds = n.lds;
   a.M = n.M; a.k = n.k;
-  a.chunks = (n.k + kBlock - 1) / kBlock * 4;
+  a.chunks = (n.k + kBlock - 1) / kBlock * (n.dtype == LORA_DTYPE_BF16 ? 4 : 8);
   a.eps = (double)n.eps;
   a.inv_k = 1.0 / (double)n.k;
+  if (plan != nullptr) {
+    if (n.dtype != LORA_DTYPE_BF16 || n.fmt == 0 || !mx_runs_plan(n.M, n.k, plan->S, true))
+      return hipErrorInvalidValue;
+    const NormShape s = norm_shape<uint16_t>(a.chunks);
+    a.log_tpr = s.log_tpr;
+    if (n.fmt == kFp8) norm_plan<kFp8>(a, s.block, *plan, st);
+    else norm_plan<kFp4>(a, s.block, *plan, st);
+    return hipGetLastError();
+  }
   if (n.dtype == LORA_DTYPE_BF16) {
     if (n.fmt == kFp8) return rmsnorm_t<uint16_t, kFp8>(a, st);
     if (n.fmt == kFp4) return rmsnorm_t<uint16_t, kFp4>(a, st);
