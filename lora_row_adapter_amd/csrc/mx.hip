@@ -114,20 +114,13 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequantize(Rows a, RowGrid g) {
 
 // v rounded to fp32 "to odd": toward zero, with the last bit set when that
 // was inexact.  A further rounding of the result to fewer bits than fp32
-// minus two is then the correct rounding of v itself, so bf16 and the 8- and
-// 4-bit codes are each rounded once from the 64-bit value.
+// minus two is then the correct rounding of v itself.
 __device__ __forceinline__ float to_odd(double v) {
   const float f = (float)v;
   const double d = (double)f;
   uint32_t b = __float_as_uint(f);
   if (d != v && !(b & 1u)) b += fabs(d) > fabs(v) ? 0xffffffffu : 1u;
   return __uint_as_float(b);
-}
-
-template <typename T>
-__device__ __forceinline__ float to_out(double v) {
-  if constexpr (sizeof(T) == 4) return (float)v;
-  else return to_odd(v);  // rounded to bf16 where it is packed
 }
 
 struct NormArgs {
@@ -182,37 +175,68 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
   auto squares = [&](const C &xv, const C &rv, double s) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
-      const double v = (double)xv.get(e) + (double)rv.get(e);
+      double v = (double)xv.get(e);
+      if (r) v += (double)rv.get(e);
       s = fma(v, v, s);
     }
     return s;
   };
   auto finish = [&](const C &xv, const C &rv, const C &wv, int64_t c, int n, double rstd) {
     C o;
-    float f[N];
-    double hv[N];
+    float hs[N], f[N];
+    // for bf16 rounded twice, to 24 and to 8 bits, but as if once: 24 >= 2 * 8 + 2
 #pragma unroll
-    for (int e = 0; e < N; ++e) hv[e] = (double)xv.get(e) + (double)rv.get(e);
+    for (int e = 0; e < N; ++e) hs[e] = xv.get(e) + rv.get(e);
     if (h != nullptr) {
 #pragma unroll
-      for (int e = 0; e < N; e += 2) o.set2(e, to_out<T>(hv[e]), to_out<T>(hv[e + 1]));
+      for (int e = 0; e < N; e += 2) o.set2(e, hs[e], hs[e + 1]);
       o.store(h, c, n);
     }
+    auto exact = [&](int e) {
+      double v = (double)xv.get(e);
+      if (r) v += (double)rv.get(e);
+      return v * rstd * (double)wv.get(e);
+    };
+    // `near` is small where a value's low 15 bits are within `kOff` of 0, that
+    // is near a value that bf16 or a code represents or a midpoint of two;
+    // below 2^-100 midpoints lie elsewhere
+    uint32_t near = ~0u;
+    float low = __builtin_inff();
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) hv[e] = hv[e] * rstd * (double)wv.get(e);
-    if (sizeof(T) == 4 && y != nullptr) {
+      for (int e = 0; e < N; ++e) {
+        f[e] = (float)exact(e);
+        near = min(near, __float_as_uint(f[e]) << 17);
+        low = fminf(low, fabsf(f[e]));
+      }
+      if (y != nullptr) {
 #pragma unroll
-      for (int e = 0; e < N; e += 2) o.set2(e, (float)hv[e], (float)hv[e + 1]);
-      o.store(y, c, n);
-    }
-    if (FMT || sizeof(T) == 2) {
+        for (int e = 0; e < N; e += 2) o.set2(e, f[e], f[e + 1]);
+        o.store(y, c, n);
+      }
+      if (FMT && (near == 0 || !(low >= 0x1p-100f))) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) f[e] = to_odd(hv[e]);
-    }
-    if (sizeof(T) == 2 && y != nullptr) {
+        for (int e = 0; e < N; ++e) f[e] = to_odd(exact(e));
+      }
+    } else {
+      constexpr uint32_t kOff = 5;  // four roundings of half a step each, relative: four steps at most
+      const float rs = rstd > 0x1p-100 && rstd < 0x1p100 ? (float)rstd : __builtin_nanf("");
 #pragma unroll
-      for (int e = 0; e < N; e += 2) o.set2(e, f[e], f[e + 1]);
-      o.store(y, c, n);
+      for (int e = 0; e < N; ++e) {
+        const float v = hs[e] * rs;
+        f[e] = v * wv.get(e);
+        near = min(near, (__float_as_uint(f[e]) + kOff) << 17);
+        low = fminf(low, fminf(fabsf(v), fabsf(f[e])));
+      }
+      if (near < (2 * kOff + 1) << 17 || !(low >= 0x1p-100f)) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) f[e] = to_odd(exact(e));
+      }
+      if (y != nullptr) {
+#pragma unroll
+        for (int e = 0; e < N; e += 2) o.set2(e, f[e], f[e + 1]);
+        o.store(y, c, n);
+      }
     }
     if constexpr (FMT != 0) {
 #pragma unroll
@@ -240,6 +264,16 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
     s = row_sum(s, a.log_tpr, red);
     if (!live) return;
     const double rstd = 1.0 / sqrt(s * a.inv_k + a.eps);
+    // past 16 elements a thread none of the sum's 64-bit values stay for the
+    // outputs: 110 registers, not 128 and 80 spilled (8192 x 8192 bf16 by 256
+    // threads a row: 127 us, not 322); up to 16 they do (112 us, not 124)
+    if constexpr (NC * N > 16) {
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        xv[i].hide();
+        rv[i].hide();
+      }
+    }
 #pragma unroll
     for (int i = 0; i < NC; ++i) {
       const int64_t c = ((int64_t)i << a.log_tpr) + lx;
@@ -351,17 +385,19 @@ hipError_t dequantize_t(const MxQuantArgs &a, hipStream_t st) {
   });
 }
 
-// Threads per row and chunks per thread (0: the row is read twice).  Two
-// chunks a thread keep most loads in flight for a workgroup that waits once:
-// 8192 x 8192 bf16 with a residual and fp8 codes takes 124 us, with one chunk
-// 140, four 130, eight 347 (registers); 64 rows 6.0, 6.1, 7.6 and 24 us.
+// Threads per row and chunks per thread (0: the row is read twice).  16
+// elements a thread keep most loads in flight for a workgroup that waits
+// once: 8192 x 8192 bf16 with a residual and fp8 codes takes 112 us, with 8
+// elements 165, 32 127; 512 rows 8.9, 11.4 and 10.4 us; 1000 x 5003 fp32
+// without a residual, fp4 codes 13.5 us, with 8 elements 18.
 struct NormShape {
   int log_tpr, nc, block;
 };
 template <typename T>
 NormShape norm_shape(int64_t chunks) {
   NormShape s;
-  s.log_tpr = log2_up((chunks + 1) / 2, Chunk<T>::kLanes == 4 ? 2 : 3, 10);
+  constexpr int nc = 16 / Chunk<T>::kElems;
+  s.log_tpr = log2_up((chunks + nc - 1) / nc, Chunk<T>::kLanes == 4 ? 2 : 3, 10);
   const int64_t per = (chunks + (int64_t(1) << s.log_tpr) - 1) >> s.log_tpr;
   s.nc = per <= 2 ? 2 : per <= 4 ? 4 : 0;
   s.block = std::max(kThreads, 1 << s.log_tpr);
