@@ -763,18 +763,29 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(device: torch.device, stream, fn, what: str, *args) -> None:
     """fn(*args, stream) with `device` current (a stream belongs to its
     device); by default on that device's current stream."""
     index = device.index
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    if index == torch.cuda.current_device():
+    if index == _current_device():
         status = fn(*args, handle)
     else:
         with torch.cuda.device(index):
             status = fn(*args, handle)
     if status != 0:
         raise LoraError(status, what)
+
+
+def _lead(t: torch.Tensor, name: str, M: int, k: int):
+    """(pointer, leading dimension) of a 2-D [M, k] tensor."""
+    ld, unit = t.stride()
+    if unit != 1 and k > 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    return t.data_ptr(), ld if M > 1 else k
 
 
 def _matrix(t: torch.Tensor, name: str, shape, dtype, device):
@@ -786,17 +797,18 @@ def _matrix(t: torch.Tensor, name: str, shape, dtype, device):
         raise ValueError("%s must be [%d, %d]" % (name, *shape))
     if t.device != device:
         raise ValueError("%s must be a tensor on %s" % (name, device))
-    ld, unit = t.stride()
-    if unit != 1 and shape[1] > 1:
-        raise ValueError("%s must have unit stride along its last dimension" % name)
-    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
+    return _lead(t, name, *shape)
 
 
-def _device_matrix(x: torch.Tensor, name: str):
-    """(shape, device) of a 2-D device tensor."""
-    if x.dim() != 2 or not x.is_cuda:
-        raise ValueError("%s must be a 2-D device tensor" % name)
-    return x.shape, x.device
+def _input(x: torch.Tensor):
+    """(dtype code, shape, device, pointer, leading dimension) of an input x."""
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % x.dtype)
+    shape = x.shape
+    if len(shape) != 2 or not x.is_cuda:
+        raise ValueError("x must be a 2-D device tensor")
+    return (dt, shape, x.device) + _lead(x, "x", *shape)
 
 
 class MX:
@@ -810,23 +822,25 @@ class MX:
         nb, width = self._sizes(fmt, k)
         if q.dtype is not torch.uint8 or scales.dtype is not torch.uint8:
             raise TypeError("q and scales must be uint8")
-        if not q.is_cuda or q.device != scales.device:
+        device, qs, ss = q.device, q.shape, scales.shape
+        if device.type != "cuda" or device != scales.device:
             raise ValueError("q and scales must be tensors on one device")
-        if q.dim() != 2 or scales.dim() != 2 or q.shape[0] != scales.shape[0]:
+        if len(qs) != 2 or len(ss) != 2 or qs[0] != ss[0]:
             raise ValueError("q and scales must be 2-D with one row per row of the matrix")
-        rows = q.shape[0]
-        if q.shape[1] < width or scales.shape[1] < nb:
+        rows, have = qs
+        if have < width or ss[1] < nb:
             raise ValueError("k = %d needs %d bytes of codes and %d scales a row" % (k, width, nb))
-        if q.stride(1) != 1 or scales.stride(1) != 1 and nb > 1:
+        (ldq, unit), (lds, sunit) = q.stride(), scales.stride()
+        if unit != 1 or sunit != 1 and nb > 1:
             raise ValueError("q and scales must have unit stride along their last dimension")
-        # a single row may have any stride; scales are read four at a time
-        ldq = q.stride(0) if rows > 1 else width
-        lds = scales.stride(0) if rows > 1 else (nb + 3) // 4 * 4
-        left = scales.untyped_storage().nbytes() - scales.storage_offset()
-        if rows > 0 and left < (rows - 1) * lds + (nb + 3) // 4 * 4:
+        read = (nb + 3) // 4 * 4  # scales are read four at a time
+        if rows <= 1:  # a single row may have any stride
+            ldq, lds = width, read
+        if ss[1] < read and rows > 0 and (scales.untyped_storage().nbytes() - scales.storage_offset() <
+                                          (rows - 1) * lds + read):
             raise ValueError("the last row of scales must have room for a multiple of 4 bytes")
         self._q, self._scales, self._own = q, scales, None
-        self._set(fmt, k, rows, q.device, q.data_ptr(), ldq, scales.data_ptr(), lds)
+        self._set(fmt, k, rows, device, q.data_ptr(), ldq, scales.data_ptr(), lds)
 
     @staticmethod
     def _sizes(fmt: int, k: int):
@@ -839,9 +853,9 @@ class MX:
         return nb, nb * (32 if fmt == MX_FP8 else 16)
 
     def _set(self, fmt, k, rows, device, q, ldq, scales, lds):
-        self.fmt, self.k, self.rows, self.device = int(fmt), int(k), rows, device
-        self._c = _CMx(self.fmt, q, ldq, scales, lds)
-        self._ref = ctypes.byref(self._c)
+        self.fmt, self.k, self.rows, self.device = fmt, k, rows, device
+        self._c = c = _CMx(fmt, q, ldq, scales, lds)
+        self._ref = ctypes.byref(c)
 
     @classmethod
     def empty(cls, rows: int, k: int, fmt: int, device="cuda") -> "MX":
@@ -874,15 +888,12 @@ class MX:
 def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = None,
                      stream=None) -> MX:
     """Microscaled x (float32 or bfloat16 [M, k])."""
-    lib = load_library()
-    dt = _dtype_code(x)
-    shape, device = _device_matrix(x, "x")
-    M, k = shape
+    lib = _lib or load_library()
+    dt, (M, k), device, xp, ldx = _input(x)
     if out is None:
         out = MX.empty(M, k, fmt, device)
     elif out.fmt != fmt or out.rows != M or out.k != k or out.device != device:
         raise ValueError("out must be a [%d, %d] matrix of this format on x's device" % (M, k))
-    xp, ldx = _matrix(x, "x", shape, x.dtype, device)
     _on(device, stream, lib.lora_mx_quantize, "lora_mx_quantize", dt, M, k, xp, ldx, out._ref)
     return out
 
@@ -890,15 +901,17 @@ def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = Non
 def lora_mx_dequantize(q: MX, dtype: torch.dtype = torch.bfloat16,
                        out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The values q stands for (float32 or bfloat16 [rows, k])."""
-    lib = load_library()
+    lib = _lib or load_library()
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
-    shape = (q.rows, q.k)
+    M, k, device = q.rows, q.k, q.device
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
-    yp, ldy = _matrix(out, "out", shape, dtype, q.device)
-    _on(q.device, stream, lib.lora_mx_dequantize, "lora_mx_dequantize", dt, q.rows, q.k, q._ref, yp, ldy)
+        out = torch.empty((M, k), dtype=dtype, device=device)
+        yp, ldy = out.data_ptr(), k
+    else:
+        yp, ldy = _matrix(out, "out", (M, k), dtype, device)
+    _on(device, stream, lib.lora_mx_dequantize, "lora_mx_dequantize", dt, M, k, q._ref, yp, ldy)
     return out
 
 
@@ -933,14 +946,12 @@ def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
                  yq: Optional[MX] = None, stream=None) -> Optional[torch.Tensor]:
     """y = h / sqrt(mean(h^2) + eps) * weight with h = x + residual; yq takes
     the normed rows microscaled.  y is made if neither is given."""
-    lib = load_library()
-    dt = _dtype_code(x)
-    shape, device = _device_matrix(x, "x")
+    lib = _lib or load_library()
+    dt, shape, device, xp, ldx = _input(x)
     dtype = x.dtype
     M, k = shape
     if y is None and yq is None:
         y = torch.empty(shape, dtype=dtype, device=device)
-    xp, ldx = _matrix(x, "x", shape, dtype, device)
     yp, ldy = (None, 0) if y is None else _matrix(y, "y", shape, dtype, device)
     if yq is not None and (yq.rows != M or yq.k != k or yq.device != device):
         raise ValueError("yq must be a [%d, %d] matrix on x's device" % (M, k))
@@ -951,15 +962,16 @@ def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
 
 def lora_gemm_mx(x: MX, W: MX, y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T on microscaled operands (bfloat16 y [rows of x, rows of W])."""
-    lib = load_library()
-    device = x.device
+    lib = _lib or load_library()
+    device, M, d = x.device, x.rows, W.rows
     if x.k != W.k or W.device != device:
         raise ValueError("x and W differ in k or device")
-    shape = (x.rows, W.rows)
     if y is None:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=device)
-    yp, ldy = _matrix(y, "y", shape, torch.bfloat16, device)
-    _on(device, stream, lib.lora_gemm_mx, "lora_gemm_mx", x.rows, x.k, W.rows, x._ref, W._ref, yp, ldy)
+        y = torch.empty((M, d), dtype=torch.bfloat16, device=device)
+        yp, ldy = y.data_ptr(), d
+    else:
+        yp, ldy = _matrix(y, "y", (M, d), torch.bfloat16, device)
+    _on(device, stream, lib.lora_gemm_mx, "lora_gemm_mx", M, x.k, d, x._ref, W._ref, yp, ldy)
     return y
 
 
@@ -983,7 +995,7 @@ def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Ten
     dtype = torch.bfloat16
     if x.dtype is not dtype:
         raise TypeError("x must be bfloat16")
-    shape, device = _device_matrix(x, "x")
+    _, shape, device, xp, ldx = _input(x)
     M, k = shape
     d_total = sum(sl.d for sl in slices)
     if W.rows != d_total or W.k != k or W.device != device:
@@ -993,7 +1005,6 @@ def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Ten
     if workspace is None:
         workspace = torch.zeros(workspace_bytes_sliced_mx(M, k, x_format, slices), dtype=torch.uint8,
                                 device=device)
-    xp, ldx = _matrix(x, "x", shape, dtype, device)
     yp, ldy = _matrix(y, "y", (M, d_total), dtype, device)
     if adapter_ids.numel() != M:
         raise ValueError("adapter_ids must have one entry per row")
