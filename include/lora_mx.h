@@ -84,9 +84,9 @@ lora_status_t lora_mx_dequantize(lora_dtype_t dtype, int64_t M, int64_t k, const
  *   y[m, j] = h[m, j] / sqrt(mean_j(h[m, j]^2) + eps) * weight[j]
  * residual_out (optional) receives h, y (optional) the normed rows, yq
  * (optional) the normed rows microscaled; y and yq may not both be NULL.
- * h and y are computed in 64 bits and each output is rounded once from
- * there, so yq does not depend on whether y is asked for, nor either on how
- * a row was split over threads, but where a sum's last bit decides a tie.
+ * Each output is what rounding the 64-bit value once gives, so yq does not
+ * depend on whether y is asked for, nor either on how a row was split over
+ * threads, but where the last bit of the 64-bit sum decides a tie.
  * All of x, residual, residual_out, weight and y are of `dtype`.  y and
  * residual_out may each be x or the residual itself (same pointer and
  * leading dimension), not both the same one; other overlaps of an output
@@ -117,7 +117,8 @@ lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
 /*
  * Bytes of workspace lora_linear_sliced_mx needs for up to max_rows rows (any
  * path, with or without a norm).  Host-only; 0 on invalid arguments.  256-byte
- * aligned, caller-owned, no initialisation needed.
+ * aligned, caller-owned, no initialisation needed (nothing here adds to
+ * lora_check's n_sync_expired: of a zero-filled workspace it stays 0).
  */
 size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_format,
                                       int32_t n_slices, const lora_slice_t *slices);

@@ -16,7 +16,7 @@ import torch
 import lora_row_adapter_amd as lr
 from lora_row_adapter_amd import workloads as wl
 import mx_ref as R
-from gpu_helpers import normwise, say
+from gpu_helpers import DevWorkload, normwise, say
 
 pytestmark = pytest.mark.gpu
 
@@ -550,3 +550,210 @@ def test_layer_captured():
         got, got_h = y.clone(), h.clone()
         want = lr.lora_linear_sliced_mx(x, W, slices, ids, norm=norm)
         assert torch.equal(got, want) and torch.equal(got_h, h)
+
+
+# ------------------------------------------------------------ the plan beside the norm or the quantising
+def more_slots(slices, S):
+    """The same adapters with unused ones behind them, S in all."""
+    out = []
+    for sl in slices:
+        ad = sl.adapters
+        n = S - ad.n_adapters
+        A = torch.cat([ad.A, torch.zeros((n,) + ad.A.shape[1:], dtype=BF, device="cuda")])
+        B = torch.cat([ad.B, torch.zeros((n,) + ad.B.shape[1:], dtype=BF, device="cuda")])
+        ranks = torch.cat([ad.ranks, torch.zeros(n, dtype=ad.ranks.dtype, device="cuda")])
+        out.append(lr.Slice(sl.d, lr.Adapters.slots(A, B, ranks), torch.cat([sl.scales, sl.scales.new_ones(n)])))
+    return out
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("with_norm", [False, True])
+@pytest.mark.parametrize("M,k", [(1, 32), (3, 256), (257, 8000), (1024, 64), (1025, 64), (4100, 2048), (70, 16384),
+                                 (70, 16392)])
+def test_layer_plan_beside_equals_a_plan_of_its_own(M, k, with_norm, fmt):
+    """Up to 64 adapters the plan is made beside the first launch: it equals
+    the one that lora_plan makes, and so do the layer's bits on that one."""
+    say("layer plan %dx%d norm %s fmt %d" % (M, k, with_norm, fmt))
+    w = wl.custom(seed=M + k, M=M, k=k, d=80, ranks=[4, 16, 64, 8], max_rank=64, none_frac=0.2)
+    slices, W, _ = layer_inputs(w)
+    x = w.x.cuda()
+    ids = w.ids.copy()
+    ids[0] = -5                      # counted, served without an adapter
+    ids = torch.from_numpy(ids).cuda()
+    norm = lr.Norm(rand(1, 1, k, BF)[0].cuda(), 1e-5, rand(2, M, k, BF).cuda()) if with_norm else None
+    for sl in (slices, more_slots(slices, 64), more_slots(slices, 65)):
+        n = lr.workspace_bytes_sliced_mx(M, k, fmt, sl)
+        ws, ws2 = (torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda") for _ in range(2))
+        y = lr.lora_linear_sliced_mx(x, W, sl, ids, x_format=fmt, norm=norm, workspace=ws)
+        report = lr.lora_check(ws)  # n_sync_expired belongs to zero-filled workspaces alone
+        assert (report["n_bad_ids"], report["n_bad_ranks"], report["n_bad_pages"]) == (1, 0, 0)
+        assert not torch.isnan(y).any()
+        lr.lora_plan(ids, sl[0].adapters, k, 80, BF, ws2)
+        for other in (ws, ws2):
+            again = lr.lora_linear_sliced_mx(x, W, sl, ids, x_format=fmt, norm=norm, workspace=other,
+                                             flags=lr.FLAG_REUSE_PLAN)
+            assert torch.equal(y, again)
+        one, two = (lr.lora_plan_view(t, M, sl[0].adapters) for t in (ws, ws2))
+        assert one.keys() == two.keys()
+        for name in one:
+            assert np.array_equal(one[name], two[name]), name
+
+
+@pytest.mark.parametrize("with_norm", [False, True])
+def test_layer_paged_adapters(with_norm):
+    """Adapters in a paged pool give the bits of the same adapters in slots."""
+    w = wl.custom(seed=21, M=90, k=512, d=320, ranks=[4, 16, 64, 8], max_rank=64, none_frac=0.2)
+    slices, W, _ = layer_inputs(w)
+    dev = DevWorkload(w, w.proj("out"), pooled=True)
+    paged = [lr.Slice(320, dev.ad, slices[0].scales)]
+    x, ids = w.x.cuda(), torch.from_numpy(w.ids).cuda()
+    norm = lr.Norm(torch.ones(512, dtype=BF, device="cuda"), 1e-5) if with_norm else None
+    ws = torch.empty(lr.workspace_bytes_sliced_mx(90, 512, lr.MX_FP8, paged), dtype=torch.uint8, device="cuda")
+    y = lr.lora_linear_sliced_mx(x, W, paged, ids, norm=norm, workspace=ws)
+    assert lr.lora_check(ws)["n_bad_pages"] == 0
+    assert torch.equal(y, lr.lora_linear_sliced_mx(x, W, slices, ids, norm=norm))
+
+
+def test_layers_on_two_streams_at_once():
+    """Two layers in flight together, a workspace each, against one after the
+    other; a captured one replayed beside an eager one."""
+    w = wl.custom(seed=31, M=200, k=1024, d=640, ranks=[8, 32, 64], max_rank=64, none_frac=0.1)
+    slices, W, _ = layer_inputs(w)
+    ids = torch.from_numpy(w.ids).cuda()
+    n = lr.workspace_bytes_sliced_mx(200, 1024, lr.MX_FP8, slices)
+    g = torch.ones(1024, dtype=BF, device="cuda")
+    sets = [(rand(i, 200, 1024, BF).cuda(), lr.Norm(g, 1e-5, rand(i + 5, 200, 1024, BF).cuda()),
+             torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(200, 640, dtype=BF, device="cuda"))
+            for i in range(2)]
+
+    def call(i):
+        x, norm, ws, y = sets[i]
+        return lr.lora_linear_sliced_mx(x, W, slices, ids, norm=norm, workspace=ws, y=y)
+
+    want = [call(i).clone() for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for rep in range(3):
+        for i in (0, 1):
+            sets[i][3].zero_()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                call(i)
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert torch.equal(sets[i][3], want[i])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0)
+    for rep in range(3):
+        for i in (0, 1):
+            sets[i][3].zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[0]):
+            graph.replay()
+        with torch.cuda.stream(streams[1]):
+            call(1)
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            assert torch.equal(sets[i][3], want[i])
+
+
+# ------------------------------------------------------------ norm: roundings at their edges
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rmsnorm_values_on_midpoints(dtype, fmt):
+    """Rows of +-1 with eps = 0 leave the weights themselves: midpoints and
+    neighbours of codes (and of bf16 values, in the sum), at every scale."""
+    k = 512
+    g = torch.Generator().manual_seed(3)
+    sign = torch.randint(0, 2, (40, k), generator=g) * 2 - 1
+    x = (sign * torch.exp2(torch.arange(40) - 20.0)[:, None]).to(dtype)
+    codes = R.code_values(fmt)[:127 if fmt == R.FP8 else 8]
+    mid = torch.from_numpy(np.concatenate([codes, (codes[:-1] + codes[1:]) / 2, codes * (1 + 2.0 ** -7)])).float()
+    w = mid[torch.randint(0, len(mid), (k,), generator=g)]
+    w = (w * torch.exp2(torch.arange(k) // 32 - 8.0)).to(dtype)
+    m = lr.MX.empty(40, k, fmt)
+    y = torch.empty(40, k, dtype=dtype, device="cuda")
+    lr.lora_rmsnorm(x.cuda(), lr.Norm(w.cuda(), 0.0), y=y, yq=m)
+    assert torch.equal(y.cpu(), (sign * w.float()).to(dtype))
+    check_norm(x, w, 0.0, None, None, y, m, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("size,weight", [(1e37, 1.0), (1e-38, 1.0), (1e-33, 1e33), (1e30, 1e-36), (1.0, 1e-38),
+                                         (1e-39, 1e-20)])
+def test_rmsnorm_far_from_one(size, weight, dtype, fmt):
+    """Magnitudes whose norm's factor, or whose product with it or with the
+    weight, leaves fp32's normal range on the way."""
+    M, k = 6, 200
+    x = (rand(5, M, k, F32, loud=0.3) * size).to(dtype)
+    r = (rand(6, M, k, F32, loud=0.3) * (size * 0.3)).to(dtype)
+    w = (rand(7, 1, k, F32, loud=0.3)[0] * weight).to(dtype)
+    h, y, m = torch.empty(M, k, dtype=dtype, device="cuda"), torch.empty(M, k, dtype=dtype, device="cuda"), \
+        lr.MX.empty(M, k, fmt)
+    lr.lora_rmsnorm(x.cuda(), lr.Norm(w.cuda(), 0.0, r.cuda(), h), y=y, yq=m)
+    check_norm(x, w, 0.0, r, h, y, m, fmt)
+
+
+def test_rmsnorm_sum_of_far_exponents():
+    """x + residual at every distance of exponents: the sum is bf16's rounding
+    of the exact one."""
+    e = torch.arange(-40, 41, dtype=torch.float64)
+    a = torch.arange(128, 256, dtype=torch.float64) / 128
+    x = (a[:, None] * torch.ones(81, dtype=torch.float64)).to(BF)
+    for seed in range(4):
+        g = torch.Generator().manual_seed(seed)
+        b = a[torch.randint(0, 128, (128, 81), generator=g)] * (torch.randint(0, 2, (128, 81), generator=g) * 2 - 1)
+        r = (b * torch.exp2(e)).to(BF)
+        h = torch.empty(128, 81, dtype=BF, device="cuda")
+        lr.lora_rmsnorm(x.cuda(), lr.Norm(torch.ones(81, dtype=BF, device="cuda"), 1e-5, r.cuda(), h))
+        # 8 bits each, 40 places apart at most: exact in 64 bits
+        want = torch.from_numpy(R.f64(x) + R.f64(r))
+        err = (torch.from_numpy(R.f64(h)) - want).abs()
+        up = torch.nextafter(h.cpu(), torch.full_like(h.cpu(), float("inf"))).double()
+        dn = torch.nextafter(h.cpu(), torch.full_like(h.cpu(), float("-inf"))).double()
+        assert ((err <= (up - want).abs()) & (err <= (dn - want).abs())).all()
+
+
+# ------------------------------------------------------------ refusals of the binding
+def test_binding_refuses_device_tensors_that_do_not_fit():
+    u = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    x = rand(1, 4, 64, BF).cuda()
+    q = lr.lora_mx_quantize(x)
+    for bad in (lambda: lr.MX(lr.MX_FP8, u(4, 32), u(4, 4), 64),            # too few codes
+                lambda: lr.MX(lr.MX_FP8, u(4, 64), u(3, 4), 64),            # rows differ
+                lambda: lr.MX(lr.MX_FP8, u(4, 64), u(4, 1), 64),            # too few scales
+                lambda: lr.MX(lr.MX_FP8, u(4, 64), u(4 * 4 - 1)[:14].as_strided((4, 2), (4, 1)), 64),
+                lambda: lr.MX(lr.MX_FP8, u(64, 4).t(), u(4, 4), 64),        # no unit stride
+                lambda: lr.MX(lr.MX_FP8, u(4, 64), u(4, 4).cpu(), 64),
+                lambda: lr.MX(lr.MX_FP8, u(256), u(4, 4), 64),
+                lambda: lr.lora_mx_quantize(x.t()),
+                lambda: lr.lora_mx_quantize(x[0]),
+                lambda: lr.lora_mx_quantize(x, lr.MX_FP4, out=q),           # another format
+                lambda: lr.lora_mx_quantize(x[:3], lr.MX_FP8, out=q),       # another size
+                lambda: lr.lora_mx_dequantize(q, out=torch.empty(4, 65, dtype=BF, device="cuda")),
+                lambda: lr.lora_mx_dequantize(q, out=torch.empty(4, 64, dtype=BF)),
+                lambda: lr.lora_rmsnorm(x, lr.Norm(torch.ones(63, dtype=BF, device="cuda"))),
+                lambda: lr.lora_rmsnorm(x, lr.Norm(torch.ones(64, dtype=BF))),
+                lambda: lr.lora_rmsnorm(x, lr.Norm(torch.ones(64, dtype=BF, device="cuda"), 1e-5, x[:3])),
+                lambda: lr.lora_gemm_mx(q, lr.MX.empty(8, 96, lr.MX_FP4))):
+        with pytest.raises(ValueError):
+            bad()
+    for bad in (lambda: lr.lora_mx_quantize(x.half()), lambda: lr.lora_mx_dequantize(q, torch.float16),
+                lambda: lr.lora_mx_dequantize(q, F32, out=torch.empty(4, 64, dtype=BF, device="cuda")),
+                lambda: lr.lora_rmsnorm(x, lr.Norm(torch.ones(64, device="cuda"))),
+                lambda: lr.MX(lr.MX_FP8, u(4, 64).char(), u(4, 4), 64)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: lr.MX(lr.MX_FP8, u(4 * 64 + 8)[8:].view(4, 64), u(4, 4), 64),  # misaligned codes
+                lambda: lr.MX(lr.MX_FP8, u(4, 72), u(4, 4), 64)):                      # rows of 72 bytes
+        with pytest.raises(lr.LoraError):
+            lr.lora_mx_quantize(x, out=bad())
+    with pytest.raises(lr.LoraError):  # the weight must be fp4
+        lr.lora_gemm_mx(q, q)
+    with pytest.raises(lr.LoraError):  # the sum and the normed rows in one place
+        lr.lora_rmsnorm(x, lr.Norm(torch.ones(64, dtype=BF, device="cuda"), 1e-5, x, x), y=x)
+    assert lr.lora_mx_quantize(x[:0]).rows == 0
+    assert lr.lora_gemm_mx(lr.lora_mx_quantize(x[:0]), lr.lora_mx_quantize(x, lr.MX_FP4)).shape == (0, 4)
