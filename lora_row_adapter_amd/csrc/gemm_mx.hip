@@ -81,11 +81,16 @@ __device__ __forceinline__ i32x4_t rsrc_words(const void *p, uint32_t bytes) {
 struct Sources {
   i32x4_t x, w, xs, ws;
 };
+// Each ends with its last row's blocks (of scales: with the four that share a
+// dword), whatever the stride.
+template <int XF>
 __device__ __forceinline__ Sources sources(const MxGemmArgs &p, int m0, int n0, int mr, int nr) {
-  Sources s = {rsrc_words(p.x + (int64_t)m0 * p.ldx, (uint32_t)(mr * p.ldx)),
-               rsrc_words(p.w + (int64_t)n0 * p.ldw, (uint32_t)(nr * p.ldw)),
-               rsrc_words(p.xs + (int64_t)m0 * p.ldxs, (uint32_t)(mr * p.ldxs)),
-               rsrc_words(p.wsc + (int64_t)n0 * p.ldws, (uint32_t)(nr * p.ldws))};
+  const int64_t sb = (p.nb + 3) & ~3;
+  const int64_t xb = (int64_t)p.nb * (XF == kFp8 ? 32 : 16), wb = (int64_t)p.nb * 16;
+  Sources s = {rsrc_words(p.x + (int64_t)m0 * p.ldx, (uint32_t)((mr - 1) * p.ldx + xb)),
+               rsrc_words(p.w + (int64_t)n0 * p.ldw, (uint32_t)((nr - 1) * p.ldw + wb)),
+               rsrc_words(p.xs + (int64_t)m0 * p.ldxs, (uint32_t)((mr - 1) * p.ldxs + sb)),
+               rsrc_words(p.wsc + (int64_t)n0 * p.ldws, (uint32_t)((nr - 1) * p.ldws + sb))};
   asm volatile("s_nop 4" : "+s"(s.x), "+s"(s.w), "+s"(s.xs), "+s"(s.ws));
   return s;
 }
@@ -158,6 +163,10 @@ __device__ __forceinline__ void store_tile(const MxGemmArgs &p, uint8_t *smem,
 // so that the eight rows a 128-byte LDS cycle serves take different banks:
 // chunk c of row r at c ^ (r & 7), in 64-byte rows at c ^ (r / 2 & 3).
 // Scales: 16 bytes a row, for four steps at a time, in a ring of their own.
+//
+// Few rows: bound by W's bytes (1 x 9216 x 8192 fp8 7 us of kernel, 40 MB) or,
+// where those are few, by the latency of a step (256 x 4096 x 4096 fp8, one
+// 64 x 64 tile a CU: 8.5 us of kernel, 0.23 a step).
 template <int BM, int BN, int WM, int WN, int KG, int KS, int ST, int XF>
 struct Tile {
   static constexpr int NW = WM * WN * KG, NT = 64 * NW;
@@ -206,7 +215,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_gemm_mx_tile(MxGemmArgs p
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int mr = min(BM, p.M - m0), nr = min(BN, p.N - n0);
-  const Sources src = sources(p, m0, n0, mr, nr);
+  const Sources src = sources<XF>(p, m0, n0, mr, nr);
   const i32x4_t rx = src.x, rw = src.w, rxs = src.xs, rws = src.ws;
   const int nk = (p.nb + 4 * KS - 1) / (4 * KS);
   const uint32_t base = lds_addr(smem);
@@ -373,6 +382,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_gemm_mx_tile(MxGemmArgs p
 // k runs in pairs of steps (256 elements).  W's ring holds two pairs, x's STX
 // tiles of 128 bytes a row: a pair in fp4, a step in fp8; scales SGB bytes a
 // row (SGB / 8 pairs), two groups.
+// 8192 x 9216 x 8192: fp4 335 us (3.7 PFLOP/s; a loop of the products on
+// registers reaches 7.1), fp8 520 (2.4; 4.8); 512 x 9216 x 8192 fp8 41 us.
+// Without the loads into LDS they take 268, 400 and 32, the loads alone 280,
+// 310 and 29: bound by neither alone, but by how far the two overlap.
 template <int BM, int BN, int WM, int WN, int STX, int SGB, int XF>
 struct Big {
   static constexpr int NW = WM * WN;
@@ -404,7 +417,7 @@ __global__ __launch_bounds__(64 * WM * WN) void k_gemm_mx_big(MxGemmArgs p) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mr = min(BM, p.M - m0), nr = min(BN, p.N - n0);
-  const Sources src = sources(p, m0, n0, mr, nr);
+  const Sources src = sources<XF>(p, m0, n0, mr, nr);
   const i32x4_t rx = src.x, rw = src.w, rxs = src.xs, rws = src.ws;
   const uint32_t ldx = (uint32_t)p.ldx, ldw = (uint32_t)p.ldw;
   const uint32_t ldxs = (uint32_t)p.ldxs, ldws = (uint32_t)p.ldws;

@@ -336,6 +336,27 @@ def test_product_into_a_wider_tensor(fmt):
         assert (out[:, :off] == 9).all() and (out[:, off + 45:] == 9).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,k,d", [(5, 96, 70), (40, 1056, 130), (300, 2080, 260)])
+def test_product_of_strided_operands_that_end_with_their_storage(M, k, d, fmt):
+    """Rows far apart, the last one's codes and scales the last bytes there
+    are; between the rows codes and scales that mean NaN."""
+    def far_apart(m):
+        nb = (k + 31) // 32
+        width, read = m.q.shape[1], (nb + 3) // 4 * 4
+        out = []
+        for t, used, pad in ((m.q, width, 48), (m.scales, read, 36)):
+            wide = torch.full(((m.rows - 1) * (used + pad) + used,), 0xFF, dtype=torch.uint8, device="cuda")
+            v = wide.as_strided((m.rows, used), (used + pad, 1))
+            v[:, :t.shape[1]] = t
+            v[:, nb if t is m.scales else used:] = 0xFF
+            out.append(v)
+        return lr.MX(m.fmt, out[0], out[1], k)
+    x, _ = random_mx(M, M, k, fmt)
+    W, _ = random_mx(d, d, k, lr.MX_FP4)
+    assert torch.equal(lr.lora_gemm_mx(far_apart(x), far_apart(W)), lr.lora_gemm_mx(x, W))
+
+
 @pytest.mark.parametrize("M", [1, 20, 70, 300])
 def test_product_keeps_nan_blocks_to_their_rows(M):
     """A NaN block of x makes its row NaN, one of W its column; nothing else."""
