@@ -110,6 +110,7 @@ lora_status_t lora_rmsnorm(lora_dtype_t dtype, int64_t M, int64_t k, const void 
  * (LORA_ERR_UNSUPPORTED otherwise), y [M, d] bf16 (ldy >= d).  Products and
  * sums run in the scaled matrix instructions with fp32 accumulators; y is
  * rounded once.  Deterministic: the summation order depends on the shape only.
+ * y must not overlap an operand (LORA_ERR_ARG).
  */
 lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
                            const lora_mx_t *W, void *y, int64_t ldy, void *stream);
@@ -130,10 +131,12 @@ size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_for
  * W: FP4, the slices' base weights stacked by rows.  x_format: the format in
  * which xn meets W (lora_mxformat_t); the adapters read xn in bf16.  With a
  * norm, residual_out receives x + residual as in lora_rmsnorm; it may be x
- * or the residual itself, and must not overlap y or the workspace.
+ * or the residual itself.  y must not overlap x, the residual or residual_out,
+ * nor any of the four the workspace (LORA_ERR_ARG).  Profiling counts the norm
+ * or quantising, and the plan beside it, with the product (LORA_K_GEMM).
  * Everything else as in lora_linear_sliced (k, ldx multiples of 8, x 16-byte
- * aligned; lora_check reports on the workspace; rows with no adapter equal
- * lora_gemm_mx of the quantised rows bitwise).
+ * aligned; lora_check reports on the workspace; up to LORA_PLAN_MAX_ROWS rows
+ * those with no adapter equal lora_gemm_mx of the quantised rows bitwise).
  */
 lora_status_t lora_linear_sliced_mx(int64_t M, int64_t k, const void *x, int64_t ldx,
                                     const lora_norm_t *norm, int32_t x_format, const lora_mx_t *W,

@@ -303,6 +303,11 @@ lora_status_t check_norm_in(lora_dtype_t dtype, int64_t M, int64_t k, const void
 lora_status_t check_norm(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, int64_t ldx,
                          const lora_norm_t *norm, const void *y, int64_t ldy, const lora_mx_t *yq);
 lora_status_t check_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *W);
+// Whether the layer's output keeps apart from x, the norm's residual and its
+// sum, and all four from the workspace.
+lora_status_t check_layer_apart(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                                const lora_norm_t *norm, const void *y, int64_t ldy, const void *workspace,
+                                size_t workspace_bytes);
 // Part of a microscaled layer's workspace behind the plan regions of a chunk
 // of `rows` rows: the quantised rows and the normed rows in bf16.
 struct MxLayout {
@@ -312,8 +317,9 @@ struct MxLayout {
 MxLayout mx_layout(int64_t rows, int64_t k, int32_t x_format);
 
 // The multi-slice layer behind lora_linear_sliced(_q, _mx) (the C ABI's types;
-// defined in lora_api.cpp).  mx: a microscaled base in place of W.  self_contained: create no library resource --
-// the plan runs on the caller's stream and no launch is timed.
+// defined in lora_api.cpp).  mx: a microscaled base in place of W.
+// self_contained: create no library resource -- the plan runs on the caller's
+// stream and no launch is timed.
 lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const void *x,
                                  int64_t ldx, const void *W, int64_t ldw, const lora_qweight_t *qw,
                                  int32_t n_slices, const lora_slice_t *slices,

@@ -462,24 +462,18 @@ lora_status_t lora_plan_view(const void *workspace, size_t workspace_bytes, int6
 namespace lora {
 // Microscaled base: host checks of what it takes in place of W.
 static lora_status_t check_mx_layer(const MxBase &mx, int64_t M, int64_t k, int64_t d,
-                                    const void *x, int64_t ldx, const void *y, int64_t ldy) {
+                                    const void *x, int64_t ldx, const void *y, int64_t ldy,
+                                    const void *workspace, size_t workspace_bytes) {
   if (mx.x_format != LORA_MX_FP8 && mx.x_format != LORA_MX_FP4) return LORA_ERR_DTYPE;
   lora_status_t s = check_gemm_mx(M, k, d, mx.W);
   if (s != LORA_OK || M == 0) return s;
   if (x == nullptr || y == nullptr) return LORA_ERR_ARG;
   if (ldx < k || ldy < d || k > (int64_t(1) << 23)) return LORA_ERR_SHAPE;
   if (k % 8 || ldx % 8 || !aligned16(x) || (uintptr_t)y % 2 != 0) return LORA_ERR_SHAPE;
-  if (mx.norm == nullptr) return LORA_OK;
-  if ((s = check_norm_in(LORA_DTYPE_BF16, M, k, x, ldx, mx.norm)) != LORA_OK) return s;
-  // y is written after every row has been normed; residual_out may be x or
-  // the residual but not the layer's output
-  const lora_norm_t &n = *mx.norm;
-  if (n.residual_out != nullptr) {
-    const uint8_t *h0 = (const uint8_t *)n.residual_out, *y0 = (const uint8_t *)y;
-    const int64_t hs = ((M - 1) * n.ldro + k) * 2, ys = ((M - 1) * ldy + d) * 2;
-    if (h0 < y0 + ys && y0 < h0 + hs) return LORA_ERR_ARG;
-  }
-  return LORA_OK;
+  if (mx.norm != nullptr && (s = check_norm_in(LORA_DTYPE_BF16, M, k, x, ldx, mx.norm)) != LORA_OK) return s;
+  // without a norm the adapters read x after y is written, and rows past the
+  // plan's are normed after the first ones' y is
+  return check_layer_apart(M, k, d, x, ldx, mx.norm, y, ldy, workspace, workspace_bytes);
 }
 
 // One chunk's rows from row c0 on: normed (where there is a norm) and
@@ -560,7 +554,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
   if (slices == nullptr || n_slices < 1 || n_slices > LORA_MAX_SLICES) return LORA_ERR_ARG;
   lora_status_t s = check_slices(n_slices, slices, M, &S, &R, &d_total);
   if (s != LORA_OK) return s;
-  s = mx   ? check_mx_layer(*mx, M, k, d_total, x, ldx, y, ldy)
+  s = mx   ? check_mx_layer(*mx, M, k, d_total, x, ldx, y, ldy, workspace, workspace_bytes)
       : qw ? check_q_gemm_args(M, k, d_total, x, ldx, qw, y, ldy)
            : check_gemm_args(dtype, M, k, d_total, x, ldx, W, ldw, y, ldy);
   if (s != LORA_OK) return s;

@@ -18,20 +18,26 @@ int64_t blocks_of(int64_t k) { return (k + 31) / 32; }
 int64_t code_bytes(int32_t fmt, int64_t k) { return blocks_of(k) * (fmt == LORA_MX_FP8 ? 32 : 16); }
 int64_t elem_bytes(lora_dtype_t t) { return t == LORA_DTYPE_BF16 ? 2 : 4; }
 
-// `rows` runs of `width` bytes, `ld` bytes apart.
+// Runs of `width` bytes, `ld` bytes apart.
 struct Span {
   const uint8_t *p;
   int64_t ld, width;
 };
+// Past its last byte, with as many rows as that (no product of a caller's
+// numbers wraps).
+unsigned __int128 end_of(const Span &s, int64_t rows) {
+  return (unsigned __int128)(uintptr_t)s.p + (unsigned __int128)(rows - 1) * (unsigned __int128)s.ld + s.width;
+}
+bool meet(const Span &a, int64_t rows_a, const Span &b, int64_t rows_b) {
+  return a.p != nullptr && b.p != nullptr && end_of(a, rows_a) > (uintptr_t)b.p && end_of(b, rows_b) > (uintptr_t)a.p;
+}
 // Whether two such regions share a byte.  With equal strides the runs are
 // compared inside one stride (columns of one wide buffer do not overlap);
 // with different ones the whole ranges are.
 bool overlap(const Span &a, const Span &b, int64_t rows) {
-  if (a.p == nullptr || b.p == nullptr) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  const uintptr_t a1 = a0 + (rows - 1) * a.ld + a.width, b1 = b0 + (rows - 1) * b.ld + b.width;
-  if (a1 <= b0 || b1 <= a0) return false;
+  if (!meet(a, rows, b, rows)) return false;
   if (a.ld == b.ld && rows > 1) {
+    const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
     const int64_t o = (int64_t)((b0 >= a0 ? b0 - a0 : a0 - b0) % (uintptr_t)a.ld);
     const int64_t first = b0 >= a0 ? a.width : b.width, second = b0 >= a0 ? b.width : a.width;
     return o < first || o + second > a.ld;
@@ -71,8 +77,7 @@ bool norm_output_apart(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, 
   for (const Span &v : {dense_span(dtype, k, x, ldx), dense_span(dtype, k, n->residual, n->ldr)})
     if (overlap(out, v, M) && !(in_place && same(out, v))) return false;
   // the weight is one row: no row of the output may meet it
-  const int64_t all = (M - 1) * out.ld + out.width, wb = k * elem_bytes(dtype);
-  return !overlap(Span{out.p, all, all}, Span{(const uint8_t *)n->weight, wb, wb}, 1);
+  return !meet(out, M, dense_span(dtype, k, n->weight, k), 1);
 }
 
 lora_status_t quant_args(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, int64_t ldx,
@@ -158,6 +163,25 @@ lora_status_t check_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *W)
   return LORA_OK;
 }
 
+lora_status_t check_layer_apart(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                                const lora_norm_t *n, const void *y, int64_t ldy, const void *workspace,
+                                size_t workspace_bytes) {
+  const lora_status_t s = check_dense(LORA_DTYPE_BF16, d, y, ldy);
+  if (s != LORA_OK) return s;
+  if (ldx > kMaxLd / 2) return LORA_ERR_SHAPE;
+  const Span out = dense_span(LORA_DTYPE_BF16, d, y, ldy);
+  const Span ws{(const uint8_t *)workspace, (int64_t)workspace_bytes, (int64_t)workspace_bytes};
+  Span others[3] = {dense_span(LORA_DTYPE_BF16, k, x, ldx), {}, {}};
+  if (n != nullptr) {
+    others[1] = dense_span(LORA_DTYPE_BF16, k, n->residual, n->ldr);
+    others[2] = dense_span(LORA_DTYPE_BF16, k, n->residual_out, n->ldro);
+  }
+  if (meet(out, M, ws, 1)) return LORA_ERR_ARG;
+  for (const Span &o : others)
+    if (overlap(out, o, M) || meet(o, M, ws, 1)) return LORA_ERR_ARG;
+  return LORA_OK;
+}
+
 MxLayout mx_layout(int64_t rows, int64_t k, int32_t x_format) {
   MxLayout L;
   L.ldq = code_bytes(x_format, k);
@@ -229,6 +253,10 @@ lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
   if ((s = check_mx(x, M, k)) != LORA_OK || M == 0) return s;
   if (x->ldq > (int64_t(1) << 23) || x->lds > (int64_t(1) << 23)) return LORA_ERR_SHAPE;
   if ((s = check_dense(LORA_DTYPE_BF16, d, y, ldy)) != LORA_OK) return s;
+  const Span out = dense_span(LORA_DTYPE_BF16, d, y, ldy);
+  if (meet(out, M, code_span(x, k), M) || meet(out, M, scale_span(x, k), M) ||
+      meet(out, M, code_span(W, k), d) || meet(out, M, scale_span(W, k), d))
+    return LORA_ERR_ARG;
   MxGemmArgs a{};
   a.xfmt = x->format;
   a.M = (int32_t)M;

@@ -227,3 +227,33 @@ def test_reference_quantiser_on_known_values():
     c, s = R.quantise(np.ones((2, 33)), R.FP4)
     assert c.shape == (2, 64) and s.shape == (2, 2) and not c[:, 33:].any()
     assert (R.dequantise(c, s, R.FP4, 33) == 1).all()
+
+
+@pytest.mark.parametrize("kw,x,W", [
+    ({"y": 1 << 20}, mx(), mx(fmt=2, q=1 << 21, scales=1 << 25)),                  # over x's codes
+    ({"y": (1 << 24) + 12}, mx(), mx(fmt=2, q=1 << 21, scales=1 << 25)),           # over x's last scales
+    ({"y": (1 << 21) - 62}, mx(), mx(fmt=2, q=1 << 21, scales=1 << 25)),           # into W's codes
+    ({"y": 1 << 25}, mx(), mx(fmt=2, q=1 << 21, scales=1 << 25)),
+    ({"M": 1 << 30, "y": 1 << 30, "ldy": 1 << 39}, mx(q=1 << 40), mx(fmt=2, q=1 << 21)),  # ranges past 64 bits
+])
+def test_gemm_refuses_an_output_over_an_operand(kw, x, W):
+    assert gemm(x, W, **kw) == ARG
+
+
+@pytest.mark.parametrize("kw", [
+    {"y": 1 << 16},                                                # y over x
+    {"y": (1 << 16) + 4 * 128 - 2},                                # the last element of x
+    {"y": 1 << 18, "n": norm(residual=1 << 18, ldr=64)},           # over the residual
+    {"y": 1 << 16, "n": norm()},
+    {"y": 1 << 30},                                                # in the workspace
+    {"x": 1 << 30},
+    {"n": norm(out=(1 << 30) + (1 << 20), ldro=64)},
+    {"n": norm(residual=(1 << 30) + (1 << 20), ldr=64)},
+])
+def test_layer_refuses_overlaps(kw):
+    assert layer(**kw) == ARG
+
+
+@pytest.mark.parametrize("kw", [{"ldy": 1 << 60}, {"ldx": 1 << 60}])
+def test_layer_refuses_strides_past_any_memory(kw):
+    assert layer(**kw) == SHAPE
