@@ -853,6 +853,7 @@ class MX:
         return nb, nb * (32 if fmt == MX_FP8 else 16)
 
     def _set(self, fmt, k, rows, device, q, ldq, scales, lds):
+        fmt, k = int(fmt), int(k)
         self.fmt, self.k, self.rows, self.device = fmt, k, rows, device
         self._c = c = _CMx(fmt, q, ldq, scales, lds)
         self._ref = ctypes.byref(c)

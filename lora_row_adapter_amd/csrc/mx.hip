@@ -60,11 +60,18 @@ __device__ __forceinline__ void quantize_rows(const Rows &a, const RowGrid &g, u
   }
 }
 
+// 9216 x 8192 fp32 to fp4 59 us (5.8 TB/s), 8192 x 4096 bf16 to fp8 18.7 us
+// (5.4 TB/s), 1 x 8192 2 us.  UNR loads a thread are in flight before the
+// first is used: with one, 69 and 21.5 us.
 template <typename T, int FMT, int UNR>
 __global__ __launch_bounds__(kThreads) void k_mx_quantize(Rows a, RowGrid g) {
   quantize_rows<T, FMT, UNR, kThreads>(a, g, blockIdx.x);
 }
 
+// The codes' values are exact in fp32, and so is their product with the scale
+// (but past fp32's range): one rounding, to bf16 where that is asked for.
+// 9216 x 8192 fp32 from fp4 48 us (7 TB/s), 8192 x 4096 bf16 from fp8 15.8
+// us (6.4 TB/s), 1 x 8192 2 us.
 template <typename T, int FMT, int UNR>
 __global__ __launch_bounds__(kThreads) void k_mx_dequantize(Rows a, RowGrid g) {
   using C = Chunk<T>;
@@ -148,9 +155,15 @@ __device__ __forceinline__ double row_sum(double s, int log_tpr, double *red) {
   return s;
 }
 
-// The rows of workgroup `block`, one per 1 << log_tpr threads.  NC > 0: each
-// thread keeps its NC chunks of x and the residual in registers, so every
-// input is read once; NC == 0: rows too long for that are read twice.
+// The rows of workgroup `block`, one per 1 << log_tpr threads:
+//   h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight.
+// The squares are summed in 64 bits (a conversion and an addition per input
+// cost about what the memory takes anyway).  The outputs are those of one
+// rounding of the 64-bit y, but computing them in 64 bits throughout costs
+// 143 us, not 112, at 8192 x 8192 bf16 with a residual (604 MB, 5.4 TB/s):
+// they are computed in fp32 and redone in 64 bits where the two could differ.
+// NC > 0: each thread keeps its NC chunks of x and the residual in registers,
+// so every input is read once; NC == 0: rows too long for that are read twice.
 template <typename T, int FMT, int NC>
 __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, double *red) {
   using C = Chunk<T>;
