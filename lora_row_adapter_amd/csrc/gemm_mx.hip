@@ -592,40 +592,85 @@ void launch_tile(MxGemmArgs a, hipStream_t st) {
                      dim3((unsigned)(a.tiles_m * a.tiles_n)), dim3(64 * WM * WN * KG), 0, st, a);
 }
 
-// The tile shape.  A shape's time is taken as s + rounds (e + c steps), with
-// rounds = its workgroups over the 256 CUs and steps of 128 elements; s, e, c
-// (us) are least-squares fits of its measured times at 96 shapes per format
-// (M 1 .. 8192 by d x k 1024 x 1024, 1024 x 8192, 4096 x 4096, 5120 x 5120,
-// 9216 x 512, 9216 x 8192), good to 2 - 10%; the choice is within 3% of the
-// best of 25 shapes tried, on the geometric mean.
-template <int XF>
+// The tile shape.  With t tiles over the 256 CUs, of which a CU holds `fit` at
+// once, and steps of 128 elements, a shape's time is taken as
+//   s + ceil(t / 256 fit) (e + c steps) + (ceil(t / 256) w + t / 256 f) steps
+// in us: what a round of workgroups takes alone, what those that share a CU
+// and those on other CUs add.  The five numbers are least-squares fits (none
+// negative) of each shape's times at up to 160 sizes per format (20 values of
+// M from 1 to 8192, d x k of 9216 x 8192, 4096 x 4096, 5120 x 5120, 2048 x
+// 4096, 1024 x 1024, 1024 x 8192, 9216 x 512 and 8192 x 1024), good to 2 - 8%;
+// the choice is within 1% of the best of 37 shapes tried, on the mean.  Of
+// those the table holds the ones without which that gets worse.  128 x 9216 x
+// 8192 fp8 takes 20.1 us (64 x 128 tiles 25), 256 x 9216 x 8192 28.6 (128 x
+// 144 tiles 41), 512 x 5120 x 5120 20.3 (28).
 struct Shape {
-  int bm, bn;
-  float s, e, c;
+  int bm, bn, fit;
+  float s, e, c, w, f;
   void (*launch)(MxGemmArgs, hipStream_t);
 };
+constexpr int fit(int smem, int waves) { return std::max(1, std::min(160 * 1024 / smem, 16 / waves)); }
 
-template <int XF>
-void launch_fmt(const MxGemmArgs &a, hipStream_t st) {
-  constexpr bool F8 = XF == kFp8;
-  static const Shape<XF> shapes[] = {
-      {16, 16, F8 ? 1.23f : 2.12f, F8 ? 1.63f : 0.74f, F8 ? 0.053f : 0.032f, launch_tile<16, 16, 1, 1, 4, 4, 8, XF>},
-      {16, 64, F8 ? 1.08f : 1.14f, F8 ? 1.88f : 1.71f, F8 ? 0.091f : 0.082f, launch_tile<16, 64, 1, 1, 4, 4, 4, XF>},
-      {32, 32, F8 ? 1.17f : 2.16f, F8 ? 1.83f : 0.72f, F8 ? 0.090f : 0.061f, launch_tile<32, 32, 1, 1, 4, 4, 4, XF>},
-      {32, 64, F8 ? 0.66f : 0.71f, F8 ? 2.39f : 2.14f, F8 ? 0.127f : 0.106f, launch_tile<32, 64, 1, 2, 4, 4, 4, XF>},
-      {64, 64, F8 ? 0.66f : 1.87f, F8 ? 2.23f : 0.97f, F8 ? 0.226f : 0.158f, launch_tile<64, 64, 2, 2, 2, 2, 4, XF>},
-      {64, 128, F8 ? 0.22f : 0.26f, F8 ? 3.03f : 2.84f, F8 ? 0.333f : 0.239f, launch_tile<64, 128, 2, 2, 2, 2, 4, XF>},
-      {128, 128, F8 ? 2.56f : 2.59f, F8 ? 1.43f : 1.55f, F8 ? 0.491f : 0.337f, launch_big<128, 128, 2, 2, 2, 16, XF>},
-      {128, 144, F8 ? 0.00f : 0.12f, F8 ? 4.74f : 4.38f, F8 ? 0.493f : 0.408f, launch_big<128, 144, 4, 1, F8 ? 3 : 2, 32, XF>},
-      {256, 192, 0.f, F8 ? 6.32f : 6.13f, F8 ? 0.974f : 0.638f, launch_big<256, 192, 4, 2, F8 ? 3 : 2, 16, XF>},
-      {256, 256, 0.f, F8 ? 6.92f : 7.71f, F8 ? 1.403f : 0.790f, launch_big<256, 256, 4, 2, 2, 16, XF>},
-  };
-  const Shape<XF> *best = nullptr;
+template <int BM, int BN, int WM, int WN, int KG, int KS, int ST, int XF>
+constexpr Shape tile(float s, float e, float c, float w, float f) {
+  using T = Tile<BM, BN, WM, WN, KG, KS, ST, XF>;
+  return {BM, BN, fit(T::SMEM, T::NW), s, e, c, w, f, launch_tile<BM, BN, WM, WN, KG, KS, ST, XF>};
+}
+template <int BM, int BN, int WM, int WN, int STX, int SGB, int XF>
+constexpr Shape big(float s, float e, float c, float w, float f) {
+  using T = Big<BM, BN, WM, WN, STX, SGB, XF>;
+  return {BM, BN, fit(T::SMEM, T::NW), s, e, c, w, f, launch_big<BM, BN, WM, WN, STX, SGB, XF>};
+}
+
+const Shape kShapes8[] = {
+    tile<16, 16, 1, 1, 4, 4, 8, kFp8>(1.28f, 1.60f, 0.054f, 0.f, 0.006f),
+    tile<16, 64, 1, 1, 4, 4, 4, kFp8>(1.18f, 1.82f, 0.086f, 0.f, 0.015f),
+    tile<32, 48, 1, 1, 4, 4, 4, kFp8>(1.24f, 2.13f, 0.102f, 0.f, 0.016f),
+    tile<32, 64, 1, 2, 4, 4, 4, kFp8>(1.10f, 2.08f, 0.112f, 0.f, 0.029f),
+    tile<32, 80, 1, 1, 4, 4, 3, kFp8>(1.30f, 2.74f, 0.159f, 0.f, 0.018f),
+    tile<48, 64, 1, 2, 4, 4, 3, kFp8>(1.21f, 2.25f, 0.149f, 0.f, 0.037f),
+    tile<64, 64, 2, 2, 2, 2, 4, kFp8>(0.94f, 2.12f, 0.201f, 0.f, 0.037f),
+    tile<64, 80, 2, 1, 2, 2, 4, kFp8>(0.87f, 2.90f, 0.227f, 0.f, 0.038f),
+    big<64, 96, 2, 2, 3, 16, kFp8>(0.89f, 2.29f, 0.173f, 0.079f, 0.063f),
+    big<64, 128, 2, 2, 3, 16, kFp8>(0.61f, 2.79f, 0.148f, 0.128f, 0.078f),
+    big<128, 96, 4, 1, 2, 32, kFp8>(1.04f, 2.54f, 0.331f, 0.036f, 0.215f),
+    big<128, 112, 4, 1, 3, 32, kFp8>(0.66f, 3.68f, 0.356f, 0.f, 0.102f),
+    big<128, 144, 4, 1, 3, 32, kFp8>(0.73f, 4.24f, 0.409f, 0.f, 0.145f),
+    big<256, 128, 4, 2, 3, 16, kFp8>(0.f, 4.64f, 0.591f, 0.f, 0.307f),
+    big<256, 160, 4, 2, 3, 16, kFp8>(0.32f, 5.12f, 0.663f, 0.f, 0.351f),
+    big<256, 192, 4, 2, 3, 16, kFp8>(0.f, 5.76f, 0.782f, 0.f, 0.398f),
+    big<256, 256, 4, 2, 2, 16, kFp8>(0.09f, 6.24f, 1.034f, 0.f, 0.676f),
+};
+const Shape kShapes4[] = {
+    tile<16, 16, 1, 1, 4, 4, 8, kFp4>(1.29f, 1.67f, 0.f, 0.035f, 0.001f),
+    tile<16, 64, 1, 1, 4, 4, 4, kFp4>(1.22f, 1.68f, 0.078f, 0.f, 0.012f),
+    tile<32, 32, 1, 1, 4, 4, 4, kFp4>(1.43f, 1.59f, 0.f, 0.060f, 0.004f),
+    tile<32, 48, 1, 1, 4, 4, 4, kFp4>(1.19f, 1.94f, 0.077f, 0.f, 0.014f),
+    tile<32, 64, 1, 2, 4, 4, 4, kFp4>(1.12f, 1.84f, 0.090f, 0.f, 0.028f),
+    tile<64, 48, 2, 1, 2, 2, 4, kFp4>(1.20f, 1.99f, 0.049f, 0.084f, 0.013f),
+    tile<64, 64, 2, 2, 2, 2, 4, kFp4>(1.02f, 1.99f, 0.007f, 0.134f, 0.027f),
+    tile<64, 80, 2, 1, 2, 4, 2, kFp4>(0.71f, 3.00f, 0.078f, 0.086f, 0.034f),
+    tile<64, 96, 2, 2, 2, 2, 4, kFp4>(0.85f, 2.40f, 0.181f, 0.f, 0.047f),
+    tile<64, 128, 2, 2, 2, 2, 4, kFp4>(0.79f, 2.61f, 0.202f, 0.f, 0.071f),
+    big<64, 128, 2, 2, 2, 16, kFp4>(0.53f, 2.71f, 0.186f, 0.041f, 0.105f),
+    big<128, 64, 4, 1, 2, 32, kFp4>(0.51f, 2.82f, 0.196f, 0.020f, 0.103f),
+    big<128, 96, 4, 1, 2, 32, kFp4>(0.75f, 3.11f, 0.196f, 0.074f, 0.098f),
+    big<128, 128, 2, 2, 2, 16, kFp4>(0.17f, 4.01f, 0.169f, 0.137f, 0.121f),
+    big<192, 128, 2, 2, 2, 16, kFp4>(0.49f, 4.17f, 0.363f, 0.f, 0.180f),
+    big<256, 160, 4, 2, 2, 16, kFp4>(0.22f, 5.01f, 0.440f, 0.f, 0.281f),
+    big<256, 192, 4, 2, 2, 16, kFp4>(0.f, 5.65f, 0.486f, 0.f, 0.312f),
+    big<256, 256, 4, 2, 2, 16, kFp4>(0.f, 6.40f, 0.627f, 0.f, 0.448f),
+};
+
+template <size_t N>
+void launch_best(const Shape (&shapes)[N], const MxGemmArgs &a, hipStream_t st) {
+  const Shape *best = nullptr;
   double least = 0;
   const double steps = (a.nb + 3) / 4;
-  for (const Shape<XF> &h : shapes) {
+  for (const Shape &h : shapes) {
     const int64_t tiles = ((int64_t)(a.M + h.bm - 1) / h.bm) * ((a.N + h.bn - 1) / h.bn);
-    const double t = h.s + (double)((tiles + 255) / 256) * (h.e + h.c * steps);
+    const double rounds = (double)((tiles + 256 * h.fit - 1) / (256 * h.fit)), cu = (double)((tiles + 255) / 256);
+    const double t = h.s + rounds * (h.e + h.c * steps) + (cu * h.w + (double)tiles / 256 * h.f) * steps;
     if (best == nullptr || t < least) {
       best = &h;
       least = t;
@@ -649,8 +694,8 @@ hipError_t launch_gemm_mx(const MxGemmArgs &all, hipStream_t st) {
       a.w += n0 * a.ldw;
       a.wsc += n0 * a.ldws;
       a.y += m0 * a.ldy + n0;
-      if (a.xfmt == kFp8) launch_fmt<kFp8>(a, st);
-      else launch_fmt<kFp4>(a, st);
+      if (a.xfmt == kFp8) launch_best(kShapes8, a, st);
+      else launch_best(kShapes4, a, st);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

@@ -294,7 +294,7 @@ def whole_mx(seed, rows, k, fmt, **kw):
 
 
 # M (rows of x), k, d: odd and ragged sizes, one row and one column, lengths
-# next to the steps of 128, 256 and 512 elements, every tile shape
+# next to the steps of 128, 256 and 512 elements
 PRODUCTS = [(1, 32, 1), (1, 1, 16), (1, 512, 48), (3, 100, 17), (16, 544, 33), (17, 480, 64), (31, 1000, 100),
             (33, 2048, 130), (48, 160, 257), (64, 640, 96), (65, 1056, 65), (100, 2000, 300), (128, 256, 144),
             (200, 384, 520), (256, 512, 288), (300, 896, 700), (513, 288, 1000), (1024, 512, 1024),
@@ -311,6 +311,20 @@ def test_product_exact_on_whole_numbers(M, k, d, fmt):
     W, Wv = whole_mx(d + k + 1, d, k, lr.MX_FP4, pad_q=32)
     y = lr.lora_gemm_mx(x, W)
     assert same_bits(y.cpu(), torch.from_numpy(X @ Wv.T).float().to(BF))
+
+
+# a size for each tile shape that the ones above do not take
+TILES8 = [(5057, 1343, 8), (4317, 653, 8), (64, 3000, 9000), (4113, 1169, 65), (4439, 730, 67), (5617, 1880, 144),
+          (130, 757, 5733), (5443, 705, 194), (788, 645, 5030), (1857, 1322, 1677), (1184, 1040, 3402),
+          (1604, 635, 3774), (2062, 641, 3904), (2466, 636, 4038), (2343, 633, 4956)]
+TILES4 = [(5146, 915, 34), (5001, 686, 33), (5572, 1503, 71), (5560, 694, 66), (423, 770, 5094), (130, 757, 5733),
+          (258, 857, 5057), (779, 641, 4812), (521, 638, 3703), (2216, 631, 1801), (1604, 635, 3774),
+          (1685, 800, 3564), (2216, 649, 3599), (3076, 670, 3124), (2507, 631, 4844)]
+
+
+@pytest.mark.parametrize("M,k,d,fmt", [t + (lr.MX_FP8,) for t in TILES8] + [t + (lr.MX_FP4,) for t in TILES4])
+def test_product_exact_on_every_tile_shape(M, k, d, fmt):
+    test_product_exact_on_whole_numbers(M, k, d, fmt)
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
