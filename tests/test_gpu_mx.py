@@ -694,6 +694,22 @@ def test_layers_on_two_streams_at_once():
             assert torch.equal(sets[i][3], want[i])
 
 
+def test_empty_batches():
+    """No rows: nothing is read, written or launched."""
+    w = wl.custom(seed=5, M=4, k=64, d=48, ranks=[8, 16], max_rank=16)
+    slices, W, _ = layer_inputs(w)
+    x, ids = w.x.cuda()[:0], torch.empty(0, dtype=torch.int32, device="cuda")
+    g = torch.ones(64, dtype=BF, device="cuda")
+    h = torch.empty_like(x)
+    m = lr.MX.empty(0, 64, lr.MX_FP8)
+    assert lr.lora_rmsnorm(x, lr.Norm(g, 1e-5, x, h), yq=m) is None
+    assert lr.lora_mx_dequantize(m).shape == (0, 64)
+    for norm in (None, lr.Norm(g, 1e-5, x, h)):
+        ws = torch.full((lr.workspace_bytes_sliced_mx(4, 64, lr.MX_FP8, slices),), 7, dtype=torch.uint8, device="cuda")
+        assert lr.lora_linear_sliced_mx(x, W, slices, ids, norm=norm, workspace=ws).shape == (0, 48)
+        assert (ws == 7).all()
+
+
 # ------------------------------------------------------------ norm: roundings at their edges
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("dtype", [BF, F32])
