@@ -935,12 +935,10 @@ class Norm:
             raise TypeError("the norm's weight must have x's dtype")
         if w.shape != shape[1:] or w.device != device or not w.is_contiguous():
             raise ValueError("the norm's weight must be a contiguous [%d] tensor on x's device" % shape[1])
-        c = _CNorm(w.data_ptr(), self.eps)
-        if self.residual is not None:
-            c.residual, c.ldr = _matrix(self.residual, "residual", shape, dtype, device)
-        if self.residual_out is not None:
-            c.residual_out, c.ldro = _matrix(self.residual_out, "residual_out", shape, dtype, device)
-        return c
+        r, out = self.residual, self.residual_out
+        rp, ldr = (None, 0) if r is None else _matrix(r, "residual", shape, dtype, device)
+        op, ldo = (None, 0) if out is None else _matrix(out, "residual_out", shape, dtype, device)
+        return _CNorm(w.data_ptr(), self.eps, rp, ldr, op, ldo)
 
 
 def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
