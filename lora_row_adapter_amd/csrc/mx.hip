@@ -160,11 +160,11 @@ __device__ __forceinline__ double row_sum(double s, int log_tpr, double *red) {
 // The squares are summed in 64 bits (a conversion and an addition per input
 // cost about what the memory takes anyway).  The outputs are those of one
 // rounding of the 64-bit y, but computing them in 64 bits throughout costs
-// 143 us, not 112, at 8192 x 8192 bf16 with a residual (604 MB, 5.4 TB/s):
+// 143 us, not 110, at 8192 x 8192 bf16 with a residual (604 MB, 5.5 TB/s):
 // they are computed in fp32 and redone in 64 bits where the two could differ.
 // NC > 0: each thread keeps its NC chunks of x and the residual in registers,
 // so every input is read once; NC == 0: rows too long for that are read twice.
-template <typename T, int FMT, int NC>
+template <typename T, int FMT, int NC, bool RES>
 __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, double *red) {
   using C = Chunk<T>;
   constexpr int N = C::kElems;
@@ -175,21 +175,20 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
   const bool live = at < a.M;
   const int64_t m = live ? at : a.M - 1;
   const T *x = (const T *)a.x + m * a.ldx;
-  const T *r = a.res ? (const T *)a.res + m * a.ldr : nullptr;
+  const T *r = RES ? (const T *)a.res + m * a.ldr : nullptr;
   const T *w = (const T *)a.w;
   T *h = a.h ? (T *)a.h + m * a.ldh : nullptr;
   T *y = a.y ? (T *)a.y + m * a.ldy : nullptr;
 
   auto load = [&](int64_t c, int n, C &xv, C &rv) {
     xv.load(x, c, n);
-    if (r) rv.load(r, c, n);
-    else rv.zero();
+    if constexpr (RES) rv.load(r, c, n);
   };
   auto squares = [&](const C &xv, const C &rv, double s) {
 #pragma unroll
     for (int e = 0; e < N; ++e) {
       double v = (double)xv.get(e);
-      if (r) v += (double)rv.get(e);
+      if constexpr (RES) v += (double)rv.get(e);
       s = fma(v, v, s);
     }
     return s;
@@ -199,7 +198,7 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
     float hs[N], f[N];
     // for bf16 rounded twice, to 24 and to 8 bits, but as if once: 24 >= 2 * 8 + 2
 #pragma unroll
-    for (int e = 0; e < N; ++e) hs[e] = xv.get(e) + rv.get(e);
+    for (int e = 0; e < N; ++e) hs[e] = RES ? xv.get(e) + rv.get(e) : xv.get(e);
     if (h != nullptr) {
 #pragma unroll
       for (int e = 0; e < N; e += 2) o.set2(e, hs[e], hs[e + 1]);
@@ -207,7 +206,7 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
     }
     auto exact = [&](int e) {
       double v = (double)xv.get(e);
-      if (r) v += (double)rv.get(e);
+      if constexpr (RES) v += (double)rv.get(e);
       return v * rstd * (double)wv.get(e);
     };
     // `near` is small where a value's low 15 bits are within `kOff` of 0, that
@@ -284,7 +283,7 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         xv[i].hide();
-        rv[i].hide();
+        if constexpr (RES) rv[i].hide();
       }
     }
 #pragma unroll
@@ -311,10 +310,10 @@ __device__ __forceinline__ void rmsnorm_rows(const NormArgs &a, uint32_t block, 
   }
 }
 
-template <typename T, int FMT, int NC>
+template <typename T, int FMT, int NC, bool RES>
 __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
   __shared__ double red[16];
-  rmsnorm_rows<T, FMT, NC>(a, blockIdx.x, red);
+  rmsnorm_rows<T, FMT, NC, RES>(a, blockIdx.x, red);
 }
 
 // The layer's plan beside the rows' work: workgroup 0 runs it, the others the
@@ -322,12 +321,12 @@ __global__ __launch_bounds__(1024) void k_rmsnorm(NormArgs a) {
 // quantising) without a stream of its own, whose fork and join cost 6 us:
 // a layer of 512 rows, 8192 -> 9216, goes from 95 to 87 us, one of 8192 rows,
 // 4096 -> 4096, from 158 to 151.
-template <int FMT, int NT>
+template <int FMT, int NT, bool RES>
 __global__ __launch_bounds__(NT) void k_rmsnorm_plan(NormArgs a, PlanArgs plan, uint32_t lds_bytes) {
   extern __shared__ __attribute__((aligned(16))) uint8_t plan_lds[];
   __shared__ double red[16];
   if (blockIdx.x == 0) plan_detail::plan_body<NT>(plan, plan_lds, lds_bytes);
-  else rmsnorm_rows<uint16_t, FMT, 2>(a, blockIdx.x - 1, red);
+  else rmsnorm_rows<uint16_t, FMT, 2, RES>(a, blockIdx.x - 1, red);
 }
 template <int FMT, int NT>
 __global__ __launch_bounds__(NT) void k_mx_quantize_plan(Rows a, RowGrid g, PlanArgs plan, uint32_t lds_bytes) {
@@ -434,9 +433,10 @@ hipError_t rmsnorm_t(NormArgs a, hipStream_t st) {
       a.sc = all.sc + m0 * a.lds;
     }
     const dim3 grid((unsigned)((a.M + rows - 1) / rows)), blk(sh.block);
-    if (sh.nc == 2) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 2>), grid, blk, 0, st, a);
-    else if (sh.nc == 4) hipLaunchKernelGGL((k_rmsnorm<T, FMT, 4>), grid, blk, 0, st, a);
-    else hipLaunchKernelGGL((k_rmsnorm<T, FMT, 0>), grid, blk, 0, st, a);
+    const auto kernel = sh.nc == 2   ? (a.res ? k_rmsnorm<T, FMT, 2, true> : k_rmsnorm<T, FMT, 2, false>)
+                        : sh.nc == 4 ? (a.res ? k_rmsnorm<T, FMT, 4, true> : k_rmsnorm<T, FMT, 4, false>)
+                                     : (a.res ? k_rmsnorm<T, FMT, 0, true> : k_rmsnorm<T, FMT, 0, false>);
+    hipLaunchKernelGGL(kernel, grid, blk, 0, st, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -454,7 +454,7 @@ template <int FMT, int NT>
 void norm_plan(const NormArgs &a, const PlanArgs &p, hipStream_t st) {
   const size_t lds = plan_detail::plan_small_lds(p.M, NT);
   const int64_t rows = NT >> a.log_tpr;
-  hipLaunchKernelGGL((k_rmsnorm_plan<FMT, NT>), dim3((unsigned)((a.M + rows - 1) / rows + 1)), dim3(NT),
+  hipLaunchKernelGGL((a.res ? k_rmsnorm_plan<FMT, NT, true> : k_rmsnorm_plan<FMT, NT, false>), dim3((unsigned)((a.M + rows - 1) / rows + 1)), dim3(NT),
                      lds, st, a, p, (uint32_t)lds);
 }
 template <int FMT>
