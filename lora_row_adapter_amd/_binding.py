@@ -780,6 +780,16 @@ def _on(device: torch.device, stream, fn, what: str, *args) -> None:
         raise LoraError(status, what)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Storage that a call makes for itself or returns, under the stream that
+    it runs on: memory of the current stream's pool may still be in use there,
+    and is handed out there again as soon as the call has dropped it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _lead(t: torch.Tensor, name: str, M: int, k: int):
     """(pointer, leading dimension) of a 2-D [M, k] tensor."""
     ld, unit = t.stride()
@@ -859,13 +869,14 @@ class MX:
         self._ref = ctypes.byref(c)
 
     @classmethod
-    def empty(cls, rows: int, k: int, fmt: int, device="cuda") -> "MX":
-        """Uninitialised storage with the least strides the library takes."""
+    def empty(cls, rows: int, k: int, fmt: int, device="cuda", stream=None) -> "MX":
+        """Uninitialised storage with the least strides the library takes, of
+        `stream` (None: the current one)."""
         nb, ldq = cls._sizes(fmt, k)
         lds = (nb + 3) // 4 * 4
         m = cls.__new__(cls)
         m._q = m._scales = None  # views of the one buffer, made when asked for
-        m._own = buf = torch.empty(rows * (ldq + lds), dtype=torch.uint8, device=device)
+        m._own = buf = _empty(rows * (ldq + lds), torch.uint8, device, stream)
         p = buf.data_ptr()
         m._set(fmt, k, rows, buf.device, p, ldq, p + rows * ldq, lds)
         return m
@@ -888,11 +899,13 @@ class MX:
 
 def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = None,
                      stream=None) -> MX:
-    """Microscaled x (float32 or bfloat16 [M, k])."""
+    """Microscaled x (float32 or bfloat16 [M, k]).  As in all calls on
+    microscaled operands, what is made with a `stream` belongs to it, as under
+    torch.cuda.stream(stream); the inputs' order is the caller's."""
     lib = _lib or load_library()
     dt, (M, k), device, xp, ldx = _input(x)
     if out is None:
-        out = MX.empty(M, k, fmt, device)
+        out = MX.empty(M, k, fmt, device, stream)
     elif out.fmt != fmt or out.rows != M or out.k != k or out.device != device:
         raise ValueError("out must be a [%d, %d] matrix of this format on x's device" % (M, k))
     _on(device, stream, lib.lora_mx_quantize, "lora_mx_quantize", dt, M, k, xp, ldx, out._ref)
@@ -908,7 +921,7 @@ def lora_mx_dequantize(q: MX, dtype: torch.dtype = torch.bfloat16,
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
     M, k, device = q.rows, q.k, q.device
     if out is None:
-        out = torch.empty((M, k), dtype=dtype, device=device)
+        out = _empty((M, k), dtype, device, stream)
         yp, ldy = out.data_ptr(), k
     else:
         yp, ldy = _matrix(out, "out", (M, k), dtype, device)
@@ -950,7 +963,7 @@ def lora_rmsnorm(x: torch.Tensor, norm: Norm, y: Optional[torch.Tensor] = None,
     dtype = x.dtype
     M, k = shape
     if y is None and yq is None:
-        y = torch.empty(shape, dtype=dtype, device=device)
+        y = _empty(shape, dtype, device, stream)
     yp, ldy = (None, 0) if y is None else _matrix(y, "y", shape, dtype, device)
     if yq is not None and (yq.rows != M or yq.k != k or yq.device != device):
         raise ValueError("yq must be a [%d, %d] matrix on x's device" % (M, k))
@@ -966,7 +979,7 @@ def lora_gemm_mx(x: MX, W: MX, y: Optional[torch.Tensor] = None, stream=None) ->
     if x.k != W.k or W.device != device:
         raise ValueError("x and W differ in k or device")
     if y is None:
-        y = torch.empty((M, d), dtype=torch.bfloat16, device=device)
+        y = _empty((M, d), torch.bfloat16, device, stream)
         yp, ldy = y.data_ptr(), d
     else:
         yp, ldy = _matrix(y, "y", (M, d), torch.bfloat16, device)
@@ -1000,10 +1013,9 @@ def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Ten
     if W.rows != d_total or W.k != k or W.device != device:
         raise ValueError("W must stack the slices' weights on x's device: [%d, %d] expected" % (d_total, k))
     if y is None:
-        y = torch.empty((M, d_total), dtype=dtype, device=device)
-    if workspace is None:
-        workspace = torch.zeros(workspace_bytes_sliced_mx(M, k, x_format, slices), dtype=torch.uint8,
-                                device=device)
+        y = _empty((M, d_total), dtype, device, stream)
+    if workspace is None:  # needs no initialisation, and lora_check sees it no more
+        workspace = _empty(workspace_bytes_sliced_mx(M, k, x_format, slices), torch.uint8, device, stream)
     yp, ldy = _matrix(y, "y", (M, d_total), dtype, device)
     if adapter_ids.numel() != M:
         raise ValueError("adapter_ids must have one entry per row")
