@@ -257,6 +257,24 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """Storage that a call makes for itself or returns, under the stream that
+    it runs on: memory of the current stream's pool may still be in use there,
+    and is handed out there again as soon as the call has dropped it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _zeros(n: int, device, stream) -> torch.Tensor:
+    """n zero bytes, likewise; the fill runs ahead of the call on its stream."""
+    if stream is None:
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
 def _dtype_code(t: torch.Tensor) -> int:
     if t.dtype not in _DTYPES:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % t.dtype)
@@ -365,10 +383,9 @@ class AdapterPool:
         c.k, c.d = self.k, self.d
         self.pool = self.page_table = self.ranks = None
         if device is not None:
-            self.pool = torch.empty(int(n_pages) * self.page_bytes, dtype=torch.uint8, device=device)
-            self.page_table = torch.empty((int(n_adapters), self.max_pages), dtype=torch.int32,
-                                          device=device)
-            self.ranks = torch.empty(int(n_adapters), dtype=torch.int32, device=device)
+            self.pool = _empty(int(n_pages) * self.page_bytes, torch.uint8, device, stream)
+            self.page_table = _empty((int(n_adapters), self.max_pages), torch.int32, device, stream)
+            self.ranks = _empty(int(n_adapters), torch.int32, device, stream)
             c.pool = self.pool.data_ptr()
             c.page_table = self.page_table.data_ptr()
             c.ranks = self.ranks.data_ptr()
@@ -527,10 +544,10 @@ def workspace_bytes(max_rows: int, d: int, k: int, dtype: torch.dtype, adapters:
 
 
 def new_workspace(max_rows: int, d: int, k: int, dtype: torch.dtype, adapters: Adapters,
-                  device=None) -> torch.Tensor:
+                  device=None, stream=None) -> torch.Tensor:
     n = workspace_bytes(max_rows, d, k, dtype, adapters)
     # zero-filled once: the library's sticky error words start at 0
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return _zeros(n, device or "cuda", stream)
 
 
 def gemm_workspace_bytes(M: int, k: int, d: int, dtype: torch.dtype) -> int:
@@ -541,10 +558,12 @@ def gemm_workspace_bytes(M: int, k: int, d: int, dtype: torch.dtype) -> int:
 def lora_gemm(x: torch.Tensor, W: torch.Tensor, y: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y = x W^T on the device (base projection only).  Without a workspace
-    one of lora_gemm_workspace_bytes bytes is allocated (torch) for the call."""
+    one of lora_gemm_workspace_bytes bytes is allocated (torch) for the call.
+    Here and in every call below, what is made with a `stream` belongs to it,
+    as under torch.cuda.stream(stream); the inputs' order is the caller's."""
     lib = load_library()
     if y is None:
-        y = torch.empty((x.shape[0], W.shape[0]), dtype=x.dtype, device=x.device)
+        y = _empty((x.shape[0], W.shape[0]), x.dtype, x.device, stream)
     xp, ldx = _rows(x, "x")
     wp, ldw = _rows(W, "W")
     yp, ldy = _rows(y, "y")
@@ -553,7 +572,7 @@ def lora_gemm(x: torch.Tensor, W: torch.Tensor, y: Optional[torch.Tensor] = None
     if workspace is None:
         n = gemm_workspace_bytes(x.shape[0], x.shape[1], W.shape[0], x.dtype)
         if n > 0:
-            workspace = torch.zeros(n, dtype=torch.uint8, device=x.device)
+            workspace = _zeros(n, x.device, stream)
     wsp, wsn = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     _check(lib.lora_gemm(_dtype_code(x), x.shape[0], x.shape[1], W.shape[0], xp, ldx, wp, ldw,
                          yp, ldy, wsp, wsn, _stream_ptr(stream)), "lora_gemm")
@@ -569,9 +588,9 @@ def lora_linear(x: torch.Tensor, W: torch.Tensor, adapters: Adapters, adapter_id
     M, k = x.shape
     d = W.shape[0]
     if y is None:
-        y = torch.empty((M, d), dtype=x.dtype, device=x.device)
+        y = _empty((M, d), x.dtype, x.device, stream)
     if workspace is None:
-        workspace = new_workspace(M, d, k, x.dtype, adapters, device=x.device)
+        workspace = new_workspace(M, d, k, x.dtype, adapters, device=x.device, stream=stream)
     xp, ldx = _rows(x, "x")
     wp, ldw = _rows(W, "W")
     yp, ldy = _rows(y, "y")
@@ -603,10 +622,9 @@ def lora_linear_sliced(x: torch.Tensor, W: torch.Tensor, slices, adapter_ids: to
     if W.shape[0] != d_total:
         raise ValueError("W must stack the slices' weights: %d rows expected" % d_total)
     if y is None:
-        y = torch.empty((M, d_total), dtype=x.dtype, device=x.device)
+        y = _empty((M, d_total), x.dtype, x.device, stream)
     if workspace is None:
-        workspace = torch.zeros(workspace_bytes_sliced(M, k, x.dtype, slices), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _zeros(workspace_bytes_sliced(M, k, x.dtype, slices), x.device, stream)
     xp, ldx = _rows(x, "x")
     wp, ldw = _rows(W, "W")
     yp, ldy = _rows(y, "y")
@@ -719,7 +737,7 @@ def lora_gemm_q(x: torch.Tensor, W: QWeight, y: Optional[torch.Tensor] = None,
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
     if y is None:
-        y = torch.empty((x.shape[0], W.d), dtype=x.dtype, device=x.device)
+        y = _empty((x.shape[0], W.d), x.dtype, x.device, stream)
     xp, ldx = _rows(x, "x")
     yp, ldy = _rows(y, "y")
     _check(lib.lora_gemm_q(x.shape[0], x.shape[1], W.d, xp, ldx, W.ref(), yp, ldy,
@@ -737,10 +755,9 @@ def lora_linear_sliced_q(x: torch.Tensor, W: QWeight, slices, adapter_ids: torch
     if W.d != d_total:
         raise ValueError("W must stack the slices' weights: %d rows expected" % d_total)
     if y is None:
-        y = torch.empty((M, d_total), dtype=x.dtype, device=x.device)
+        y = _empty((M, d_total), x.dtype, x.device, stream)
     if workspace is None:
-        workspace = torch.zeros(workspace_bytes_sliced(M, k, x.dtype, slices), dtype=torch.uint8,
-                                device=x.device)
+        workspace = _zeros(workspace_bytes_sliced(M, k, x.dtype, slices), x.device, stream)
     xp, ldx = _rows(x, "x")
     yp, ldy = _rows(y, "y")
     if adapter_ids.numel() != M:
@@ -778,16 +795,6 @@ def _on(device: torch.device, stream, fn, what: str, *args) -> None:
             status = fn(*args, handle)
     if status != 0:
         raise LoraError(status, what)
-
-
-def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
-    """Storage that a call makes for itself or returns, under the stream that
-    it runs on: memory of the current stream's pool may still be in use there,
-    and is handed out there again as soon as the call has dropped it."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _lead(t: torch.Tensor, name: str, M: int, k: int):
@@ -899,9 +906,7 @@ class MX:
 
 def lora_mx_quantize(x: torch.Tensor, fmt: int = MX_FP8, out: Optional[MX] = None,
                      stream=None) -> MX:
-    """Microscaled x (float32 or bfloat16 [M, k]).  As in all calls on
-    microscaled operands, what is made with a `stream` belongs to it, as under
-    torch.cuda.stream(stream); the inputs' order is the caller's."""
+    """Microscaled x (float32 or bfloat16 [M, k])."""
     lib = _lib or load_library()
     dt, (M, k), device, xp, ldx = _input(x)
     if out is None:
@@ -1037,7 +1042,7 @@ def lora_merge(W: torch.Tensor, adapters: Adapters, adapter: int, scales: torch.
     """W' = W + coef * scales[adapter] * B_a A_a (out=W merges in place)."""
     lib = load_library()
     if out is None:
-        out = torch.empty_like(W)
+        out = _empty(W.shape, W.dtype, W.device, stream)
     wp, ldw = _rows(W, "W")
     op, ldo = _rows(out, "out")
     if out.dtype != W.dtype or out.shape != W.shape:
@@ -1056,7 +1061,7 @@ def lora_translate(adapters: Adapters, adapter: torch.Tensor, logical_off: torch
     n = adapter.numel()
     if logical_off.numel() != n:
         raise ValueError("adapter and logical_off differ in length")
-    out = torch.empty(n, dtype=torch.int64, device=adapter.device)
+    out = _empty(n, torch.int64, adapter.device, stream)
     _check(lib.lora_translate(adapters.ref(), _dev(adapter, "adapter", torch.int32),
                               _dev(logical_off, "logical_off", torch.int64), n,
                               _dev(out, "phys_off"), _stream_ptr(stream)), "lora_translate")

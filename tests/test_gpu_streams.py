@@ -76,3 +76,25 @@ def test_microscaled_calls_beside_a_busy_stream():
         lambda s: [lr.lora_linear_sliced_mx(x, W, slices, ids, norm=norm, stream=s)],
         lambda s: [lr.lora_linear_sliced_mx(x, W, slices, ids, x_format=lr.MX_FP4, stream=s)],
     ])
+
+
+def test_dense_and_quantised_calls_beside_a_busy_stream():
+    w = wl.custom(seed=4, M=200, k=1024, d=640, ranks=[8, 32, 64], max_rank=64, none_frac=0.1)
+    p = w.proj("out")
+    A, Bm = wl.slots(w, p)
+    ad = lr.Adapters.slots(A.cuda(), Bm.cuda(), torch.from_numpy(w.ranks).cuda())
+    scales = torch.from_numpy(w.scales).cuda()
+    slices = [lr.Slice(640, ad, scales)]
+    x, ids, W = w.x.cuda(), torch.from_numpy(w.ids).cuda(), p.W.cuda()
+    g = torch.Generator().manual_seed(5)
+    Q = lr.QWeight(lr.W_INT8, torch.randint(-127, 128, (640, 1024), generator=g, dtype=torch.int8).cuda(),
+                   torch.full((640,), 0.01, device="cuda"), 1024)
+    say("dense and quantised calls beside a busy stream")
+    check_beside_busy([
+        lambda s: [lr.lora_gemm(x, W, stream=s)],
+        lambda s: [lr.lora_linear(x, W, ad, ids, scales, stream=s)],
+        lambda s: [lr.lora_linear_sliced(x, W, slices, ids, stream=s)],
+        lambda s: [lr.lora_gemm_q(x, Q, stream=s)],
+        lambda s: [lr.lora_linear_sliced_q(x, Q, slices, ids, stream=s)],
+        lambda s: [lr.lora_merge(W, ad, 1, scales, stream=s)],
+    ])

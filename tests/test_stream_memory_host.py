@@ -108,3 +108,56 @@ def test_microscaled_calls_make_their_tensors_under_their_stream(name, made):
 def test_microscaled_layer_fills_no_workspace(made):
     MX_CALLS["layer"][1](None)
     assert [f for f, _ in made] == ["empty", "empty"]
+
+
+def adapters():
+    return SimpleNamespace(kind=B.KIND_POOL, ref=lambda: None)
+
+
+def qweight():
+    return SimpleNamespace(d=8, ref=lambda: None)
+
+
+def x():
+    return Tensor((4, 64))
+
+
+def ids():
+    return Tensor(4, torch.int32)
+
+
+CALLS = {
+    "gemm": (2, lambda s: lr.lora_gemm(x(), Tensor((8, 64)), stream=s)),
+    "linear": (2, lambda s: lr.lora_linear(x(), Tensor((8, 64)), adapters(), ids(), Tensor(4, torch.float32), stream=s)),
+    "sliced": (2, lambda s: lr.lora_linear_sliced(x(), Tensor((8, 64)), SLICES, ids(), stream=s)),
+    "gemm_q": (1, lambda s: lr.lora_gemm_q(x(), qweight(), stream=s)),
+    "sliced_q": (2, lambda s: lr.lora_linear_sliced_q(x(), qweight(), SLICES, ids(), stream=s)),
+    "merge": (1, lambda s: lr.lora_merge(Tensor((8, 64)), adapters(), 0, Tensor(4, torch.float32), stream=s)),
+    "translate": (1, lambda s: lr.lora_translate(adapters(), ids(), Tensor(4, torch.int64), stream=s)),
+}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_calls_make_their_tensors_under_their_stream(name, made):
+    n, call = CALLS[name]
+    call(SIDE)
+    assert [s for _, s in made] == ["side"] * n
+    made.clear()
+    call(None)
+    assert [s for _, s in made] == ["current"] * n
+
+
+@pytest.mark.parametrize("name", ["gemm", "linear", "sliced", "sliced_q"])
+def test_dense_workspaces_are_zero_filled(name, made):
+    """The split-K base product counts expired waits from 0 on."""
+    CALLS[name][1](None)
+    assert [f for f, _ in made] == ["empty", "zeros"]
+
+
+def test_a_pool_is_made_under_its_stream(made, monkeypatch):
+    real = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype=None, device=None: Tensor(
+        shape, dtype) if shape == () else real(shape, dtype=dtype, device=device))
+    monkeypatch.setattr(Tensor, "element_size", lambda self: 2, raising=False)
+    lr.AdapterPool(4, 1024, 2, 2, 8, 64, 64, device=DEV, stream=SIDE)
+    assert [s for _, s in made] == ["side"] * 3
