@@ -132,8 +132,9 @@ size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_for
  * which xn meets W (lora_mxformat_t); the adapters read xn in bf16.  With a
  * norm, residual_out receives x + residual as in lora_rmsnorm; it may be x
  * or the residual itself.  y must not overlap x, the residual or residual_out,
- * nor any of the four the workspace (LORA_ERR_ARG).  Profiling counts the norm
- * or quantising, and the plan beside it, with the product (LORA_K_GEMM).
+ * nor any of the four the workspace, nor y, residual_out or the workspace W or
+ * the norm's weight (LORA_ERR_ARG).  Profiling counts the norm or quantising,
+ * and the plan beside it, with the product (LORA_K_GEMM).
  * Everything else as in lora_linear_sliced (k, ldx multiples of 8, x 16-byte
  * aligned; lora_check reports on the workspace; up to LORA_PLAN_MAX_ROWS rows
  * those with no adapter equal lora_gemm_mx of the quantised rows bitwise).

@@ -304,10 +304,11 @@ lora_status_t check_norm(lora_dtype_t dtype, int64_t M, int64_t k, const void *x
                          const lora_norm_t *norm, const void *y, int64_t ldy, const lora_mx_t *yq);
 lora_status_t check_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *W);
 // Whether the layer's output keeps apart from x, the norm's residual and its
-// sum, and all four from the workspace.
+// sum, all four from the workspace, and what is written from W and the norm's
+// weight.
 lora_status_t check_layer_apart(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                                const lora_norm_t *norm, const void *y, int64_t ldy, const void *workspace,
-                                size_t workspace_bytes);
+                                const lora_norm_t *norm, const lora_mx_t *W, const void *y, int64_t ldy,
+                                const void *workspace, size_t workspace_bytes);
 // Part of a microscaled layer's workspace behind the plan regions of a chunk
 // of `rows` rows: the quantised rows and the normed rows in bf16.
 struct MxLayout {

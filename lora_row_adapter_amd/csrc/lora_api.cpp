@@ -473,7 +473,7 @@ static lora_status_t check_mx_layer(const MxBase &mx, int64_t M, int64_t k, int6
   if (mx.norm != nullptr && (s = check_norm_in(LORA_DTYPE_BF16, M, k, x, ldx, mx.norm)) != LORA_OK) return s;
   // without a norm the adapters read x after y is written, and rows past the
   // plan's are normed after the first ones' y is
-  return check_layer_apart(M, k, d, x, ldx, mx.norm, y, ldy, workspace, workspace_bytes);
+  return check_layer_apart(M, k, d, x, ldx, mx.norm, mx.W, y, ldy, workspace, workspace_bytes);
 }
 
 // One chunk's rows from row c0 on: normed (where there is a norm) and

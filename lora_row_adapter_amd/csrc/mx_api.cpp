@@ -164,8 +164,8 @@ lora_status_t check_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *W)
 }
 
 lora_status_t check_layer_apart(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                                const lora_norm_t *n, const void *y, int64_t ldy, const void *workspace,
-                                size_t workspace_bytes) {
+                                const lora_norm_t *n, const lora_mx_t *W, const void *y, int64_t ldy,
+                                const void *workspace, size_t workspace_bytes) {
   const lora_status_t s = check_dense(LORA_DTYPE_BF16, d, y, ldy);
   if (s != LORA_OK) return s;
   if (ldx > kMaxLd / 2) return LORA_ERR_SHAPE;
@@ -179,6 +179,11 @@ lora_status_t check_layer_apart(int64_t M, int64_t k, int64_t d, const void *x, 
   if (meet(out, M, ws, 1)) return LORA_ERR_ARG;
   for (const Span &o : others)
     if (overlap(out, o, M) || meet(o, M, ws, 1)) return LORA_ERR_ARG;
+  // (the norm's sum keeps apart from its weight: check_norm_in)
+  const Span weight = n != nullptr ? dense_span(LORA_DTYPE_BF16, k, n->weight, k) : Span{};
+  if (meet(weight, 1, out, M) || meet(weight, 1, ws, 1)) return LORA_ERR_ARG;
+  for (const Span &w : {code_span(W, k), scale_span(W, k)})
+    if (meet(w, d, out, M) || meet(w, d, ws, 1) || meet(w, d, others[2], M)) return LORA_ERR_ARG;
   return LORA_OK;
 }
 

@@ -257,3 +257,26 @@ def test_layer_refuses_overlaps(kw):
 @pytest.mark.parametrize("kw", [{"ldy": 1 << 60}, {"ldx": 1 << 60}])
 def test_layer_refuses_strides_past_any_memory(kw):
     assert layer(**kw) == SHAPE
+
+
+APART = mx(fmt=2, q=1 << 40, ldq=32, scales=1 << 41)
+
+
+@pytest.mark.parametrize("kw", [
+    {"y": 1 << 40},                                                # y over W's codes
+    {"y": (1 << 40) + 8 * 32 - 2},                                 # their last bytes
+    {"y": (1 << 40) - 4 * 16 + 2},                                 # y's last element over their first byte
+    {"y": 1 << 41},                                                # over W's scales
+    {"y": (1 << 41) + 7 * 4},                                      # the last row's
+    {"ws": 1 << 40},
+    {"ws": (1 << 41) - (1 << 28) + 256},
+    {"n": norm(out=1 << 40, ldro=64)},                             # the residual's sum over W
+    {"n": norm(out=(1 << 41) + 16, ldro=64)},
+    {"y": 1 << 28, "n": norm()},                                   # y over the norm's weight
+    {"y": (1 << 28) + 126, "n": norm()},
+    {"ws": 1 << 28, "ws_bytes": 1 << 20, "n": norm()},
+    {"n": norm(out=1 << 28, ldro=64)},
+])
+def test_layer_refuses_outputs_over_its_weights(kw):
+    kw = dict({"ws": 1 << 45}, **kw)
+    assert layer(W=APART, **kw) == ARG
