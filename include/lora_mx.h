@@ -86,7 +86,9 @@ lora_status_t lora_mx_dequantize(lora_dtype_t dtype, int64_t M, int64_t k, const
  * (optional) the normed rows microscaled; y and yq may not both be NULL.
  * Each output is what rounding the 64-bit value once gives, so yq does not
  * depend on whether y is asked for, nor either on how a row was split over
- * threads, but where the last bit of the 64-bit sum decides a tie.
+ * threads, but where the last bit of the 64-bit sum decides a tie.  A normed
+ * value that fp32 rounds to an infinity is one for yq too: its block gets
+ * s = 255.
  * All of x, residual, residual_out, weight and y are of `dtype`.  y and
  * residual_out may each be x or the residual itself (same pointer and
  * leading dimension), not both the same one; other overlaps of an output

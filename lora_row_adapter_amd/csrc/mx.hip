@@ -121,12 +121,13 @@ __global__ __launch_bounds__(kThreads) void k_mx_dequantize(Rows a, RowGrid g) {
 
 // v rounded to fp32 "to odd": toward zero, with the last bit set when that
 // was inexact.  A further rounding of the result to fewer bits than fp32
-// minus two is then the correct rounding of v itself.
+// minus two is then the correct rounding of v itself.  What rounds to nearest
+// as an infinity is one (and its block's scale NaN, as its value in fp32).
 __device__ __forceinline__ float to_odd(double v) {
   const float f = (float)v;
   const double d = (double)f;
   uint32_t b = __float_as_uint(f);
-  if (d != v && !(b & 1u)) b += fabs(d) > fabs(v) ? 0xffffffffu : 1u;
+  if (d != v && !(b & 1u) && fabsf(f) < __builtin_inff()) b += fabs(d) > fabs(v) ? 0xffffffffu : 1u;
   return __uint_as_float(b);
 }
 

@@ -808,3 +808,36 @@ def test_binding_refuses_device_tensors_that_do_not_fit():
         lr.lora_rmsnorm(x, lr.Norm(torch.ones(64, dtype=BF, device="cuda"), 1e-5, x, x), y=x)
     assert lr.lora_mx_quantize(x[:0]).rows == 0
     assert lr.lora_gemm_mx(lr.lora_mx_quantize(x[:0]), lr.lora_mx_quantize(x, lr.MX_FP4)).shape == (0, 4)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("k", [1023, 1024, 40001])
+def test_rmsnorm_values_past_fp32(k, dtype, fmt):
+    """A row with one element other than 0 leaves sqrt(k) times its weight:
+    values next to and past fp32's largest.  What rounds to an infinity there
+    is one for the codes as for y, and its neighbours keep theirs."""
+    M = 9
+    at = np.arange(M) * 40 % k                     # one block or two apart
+    x = torch.zeros(M, k, dtype=dtype)
+    w = torch.ones(k, dtype=dtype)
+    root = 2.0 ** np.floor(np.log2(np.sqrt(k)))
+    for m in range(M):
+        x[m, at[m]] = -3.0 if m % 2 else 3.0
+        # (for k = 1024, row 3: the largest bf16; row 6: 2^128)
+        w[at[m]] = [2.0 ** 120, 2.0 ** 127, 2.0 ** 127 * (1 + 126 / 128), 2.0 ** 127 * (1 + 127 / 128), 2.0 ** 126,
+                    2.0 ** 124 * 1.5, 2.0 ** 128, 2.0 ** 129, 2.0 ** 130][m] / root
+    y, m = torch.empty(M, k, dtype=dtype, device="cuda"), lr.MX.empty(M, k, fmt)
+    lr.lora_rmsnorm(x.cuda(), lr.Norm(w.cuda(), 0.0), y=y, yq=m)
+    _, Y = R.rmsnorm(R.f64(x), R.f64(w), 0.0)
+    edge = 2.0 ** 128 - 2.0 ** 103                 # halfway from the largest fp32 to 2^128
+    assert (np.abs(Y).max(1) >= edge).any() and (np.abs(np.abs(Y) / edge - 1) > 1e-12).all()
+    c, s = codes_of(m)
+    want_c, want_s = R.quantise(np.where(np.abs(Y) < edge, Y, np.copysign(np.inf, Y)), fmt)
+    assert np.array_equal(s, want_s) and np.array_equal(c, want_c)
+    half = 2.0 ** 128 - (2.0 ** 119 if dtype is BF else 2.0 ** 103)
+    assert np.array_equal(np.isinf(R.f64(y)), np.abs(Y) >= half)
+    m2 = lr.MX.empty(M, k, fmt)                    # and with a residual
+    lr.lora_rmsnorm(x.cuda(), lr.Norm(w.cuda(), 0.0, torch.zeros_like(x).cuda()), yq=m2)
+    c2, s2 = codes_of(m2)
+    assert np.array_equal(s2, want_s) and np.array_equal(c2, want_c)
