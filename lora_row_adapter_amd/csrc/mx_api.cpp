@@ -284,7 +284,9 @@ size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_for
                                       int32_t n_slices, const lora_slice_t *slices) {
   if (x_format != LORA_MX_FP8 && x_format != LORA_MX_FP4) return 0;
   if (max_rows < 0 || k < 1 || k > INT32_MAX) return 0;
-  const size_t plan = lora_workspace_bytes_sliced(max_rows, k, LORA_DTYPE_BF16, n_slices, slices);
+  // the plan's regions alone, which depend on no type: in fp32 the dense base
+  // product, which this layer does not run, takes none of its own
+  const size_t plan = lora_workspace_bytes_sliced(max_rows, k, LORA_DTYPE_F32, n_slices, slices);
   if (plan == 0) return 0;
   const int64_t rows = std::min<int64_t>(std::max<int64_t>(max_rows, 1), kPlanMaxRows);
   return plan + mx_layout(rows, k, x_format).total;

@@ -280,3 +280,18 @@ APART = mx(fmt=2, q=1 << 40, ldq=32, scales=1 << 41)
 def test_layer_refuses_outputs_over_its_weights(kw):
     kw = dict({"ws": 1 << 45}, **kw)
     assert layer(W=APART, **kw) == ARG
+
+
+@pytest.mark.parametrize("M,k,d", [(4, 64, 8), (512, 8192, 9216), (256, 4096, 1024), (8192, 4096, 4096), (1, 8192, 9216)])
+def test_layer_workspace_is_what_the_layer_checks_for(M, k, d):
+    """Not a byte more: one less is refused, also at sizes where the dense
+    layer's workspace has a region for its base product."""
+    lib = lr.load_library()
+    sl = slices(d=d)
+    for fmt in (1, 2):
+        n = lib.lora_workspace_bytes_sliced_mx(M, k, fmt, 1, sl)
+        own = sum((v + 255) // 256 * 256 for v in (M * k // fmt, M * k // 32, 2 * M * k))
+        assert n == lib.lora_workspace_bytes_sliced(M, k, 0, 1, sl) + own  # fp32: the plan's regions
+        short = dict(M=M, k=k, ldx=k, fmt=fmt, W=mx(fmt=2, ldq=k // 2, lds=max(k // 32, 4), q=1 << 40, scales=1 << 41),
+                     sl=sl, ldy=d, x=1 << 33, y=1 << 34, ws=1 << 45)
+        assert layer(ws_bytes=n - 1, **short) == WORKSPACE
