@@ -34,6 +34,9 @@
  * Conventions as in lora_row.h: device pointers, row-major, asynchronous on
  * `stream`, errors as lora_status_t, no device allocation, safe to capture
  * into a graph.  M == 0 is a no-op.  Row counts, k and d are at most 2^31 - 1.
+ * lora_profile_* times the product (LORA_K_GEMM) and the layer; quantising,
+ * reading back and the norm called by themselves have no class and are not
+ * timed.
  */
 #ifndef LORA_MX_H
 #define LORA_MX_H

@@ -296,6 +296,18 @@ struct MxBase {
   int32_t x_format;
   const lora_norm_t *norm;
 };
+// Optional per-kernel timing (lora_profile_*; defined in lora_api.cpp).
+namespace prof {
+int begin(int c, hipStream_t st);
+void end(int i, hipStream_t st);
+}  // namespace prof
+template <typename F>
+hipError_t timed(int c, hipStream_t st, F &&launch) {
+  const int slot = prof::begin(c, st);
+  const hipError_t e = launch();
+  prof::end(slot, st);
+  return e;
+}
 // Host checks shared by the entry points (mx_api.cpp).
 lora_status_t check_mx(const lora_mx_t *m, int64_t rows, int64_t k);
 lora_status_t check_norm_in(lora_dtype_t dtype, int64_t M, int64_t k, const void *x, int64_t ldx,

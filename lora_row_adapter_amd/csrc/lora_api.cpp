@@ -139,13 +139,6 @@ bool get(hipStream_t *s, hipEvent_t *fork, hipEvent_t *join) {
 }  // namespace side
 
 
-template <typename F>
-static hipError_t timed(int c, hipStream_t st, F &&launch) {
-  const int slot = prof::begin(c, st);
-  const hipError_t e = launch();
-  prof::end(slot, st);
-  return e;
-}
 // timed() unless the call must not create the profiler's events
 template <typename F>
 static hipError_t maybe_timed(bool untimed, int c, hipStream_t st, F &&launch) {

@@ -277,7 +277,8 @@ lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
   a.ldws = W->lds;
   a.y = (uint16_t *)y;
   a.ldy = ldy;
-  return launch_gemm_mx(a, (hipStream_t)stream) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+  const hipError_t e = timed(LORA_K_GEMM, (hipStream_t)stream, [&] { return launch_gemm_mx(a, (hipStream_t)stream); });
+  return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
 size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_format,

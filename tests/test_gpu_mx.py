@@ -841,3 +841,22 @@ def test_rmsnorm_values_past_fp32(k, dtype, fmt):
     lr.lora_rmsnorm(x.cuda(), lr.Norm(w.cuda(), 0.0, torch.zeros_like(x).cuda()), yq=m2)
     c2, s2 = codes_of(m2)
     assert np.array_equal(s2, want_s) and np.array_equal(c2, want_c)
+
+
+def test_profiler_times_the_product_and_the_layer():
+    """One launch of the base product's class each; the row operators called by
+    themselves have no class."""
+    w = wl.custom(seed=6, M=20, k=256, d=96, ranks=[8], max_rank=8)
+    slices, W, _ = layer_inputs(w)
+    x, ids = w.x.cuda(), torch.from_numpy(w.ids).cuda()
+    with lr.Profiler():
+        m = lr.lora_mx_quantize(x)
+        lr.lora_rmsnorm(x, lr.Norm(torch.ones(256, dtype=BF, device="cuda")), yq=m)
+        lr.lora_mx_dequantize(m)
+        assert all(lr.Profiler.read()[c]["launches"] == 0 for c in lr.KERNEL_CLASSES)
+        lr.lora_gemm_mx(m, W)
+        one = lr.Profiler.read()
+        lr.lora_linear_sliced_mx(x, W, slices, ids)
+        two = lr.Profiler.read(reset=True)
+    assert one["gemm"]["launches"] == 1 and one["gemm"]["ms"] > 0
+    assert two["gemm"]["launches"] == 2 and two["sgmv_shrink"]["launches"] == 1 == two["sgmv_expand"]["launches"]
