@@ -121,6 +121,15 @@ lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
                            const lora_mx_t *W, void *y, int64_t ldy, void *stream);
 
 /*
+ * Testing hook: which of the product's tile shapes a size takes (their order
+ * is the library's own; -1: invalid arguments).  Host-only.  out[0], out[1]:
+ * the tile's rows of x and of W; out[2]: the elements of k that the longest
+ * of the kernel's LDS rings holds (past them all have been refilled).
+ */
+int32_t lora_test_gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t x_format,
+                                int32_t out[3]);
+
+/*
  * Bytes of workspace lora_linear_sliced_mx needs for up to max_rows rows (any
  * path, with or without a norm).  Host-only; 0 on invalid arguments.  256-byte
  * aligned, caller-owned, no initialisation needed (nothing here adds to

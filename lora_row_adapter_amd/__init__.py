@@ -12,6 +12,6 @@ from ._binding import (  # noqa: F401
     LoraError, Profiler, Slice, abi_version, library_path, load_library, lora_check, lora_gemm,
     lora_linear, lora_linear_sliced, lora_linear_sliced_noalloc, NOALLOC_SCRATCH_BYTES, lora_merge, lora_plan, lora_plan_view, lora_translate, new_workspace,
     status_str, workspace_bytes, workspace_bytes_sliced, gemm_workspace_bytes, test_sync_spin_limit,
-    MX, MX_FP4, MX_FP8, Norm, lora_gemm_mx, lora_linear_sliced_mx, lora_mx_dequantize,
+    MX, MX_FP4, MX_FP8, Norm, test_gemm_mx_shape, lora_gemm_mx, lora_linear_sliced_mx, lora_mx_dequantize,
     lora_mx_quantize, lora_rmsnorm, workspace_bytes_sliced_mx,
 )

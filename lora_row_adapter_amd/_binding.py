@@ -193,6 +193,8 @@ def load_library():
     lib.lora_rmsnorm.restype = i32
     lib.lora_gemm_mx.argtypes = [i64, i64, i64, pmx, pmx, p, i64, p]
     lib.lora_gemm_mx.restype = i32
+    lib.lora_test_gemm_mx_shape.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i32)]
+    lib.lora_test_gemm_mx_shape.restype = i32
     lib.lora_workspace_bytes_sliced_mx.argtypes = [i64, i64, i32, i32, psl]
     lib.lora_workspace_bytes_sliced_mx.restype = sz
     lib.lora_linear_sliced_mx.argtypes = [i64, i64, p, i64, pno, i32, pmx, i32, psl, p, p, i64, p,
@@ -990,6 +992,16 @@ def lora_gemm_mx(x: MX, W: MX, y: Optional[torch.Tensor] = None, stream=None) ->
         yp, ldy = _matrix(y, "y", (M, d), torch.bfloat16, device)
     _on(device, stream, lib.lora_gemm_mx, "lora_gemm_mx", M, x.k, d, x._ref, W._ref, yp, ldy)
     return y
+
+
+def test_gemm_mx_shape(M: int, k: int, d: int, x_format: int):
+    """Testing hook: (index, rows, columns, ring) of the tile shape that
+    lora_gemm_mx takes; ring: elements of k that its longest LDS ring holds."""
+    out = (ctypes.c_int32 * 3)()
+    i = load_library().lora_test_gemm_mx_shape(int(M), int(k), int(d), int(x_format), out)
+    if i < 0:
+        raise LoraError(1, "lora_test_gemm_mx_shape")
+    return (i,) + tuple(out)
 
 
 def workspace_bytes_sliced_mx(max_rows: int, k: int, x_format: int, slices) -> int:

@@ -606,6 +606,7 @@ void launch_tile(MxGemmArgs a, hipStream_t st) {
 // 144 tiles 41), 512 x 5120 x 5120 20.3 (28).
 struct Shape {
   int bm, bn, fit;
+  int ring;  // elements of k that the longest LDS ring holds
   float s, e, c, w, f;
   void (*launch)(MxGemmArgs, hipStream_t);
 };
@@ -614,12 +615,13 @@ constexpr int fit(int smem, int waves) { return std::max(1, std::min(160 * 1024 
 template <int BM, int BN, int WM, int WN, int KG, int KS, int ST, int XF>
 constexpr Shape tile(float s, float e, float c, float w, float f) {
   using T = Tile<BM, BN, WM, WN, KG, KS, ST, XF>;
-  return {BM, BN, fit(T::SMEM, T::NW), s, e, c, w, f, launch_tile<BM, BN, WM, WN, KG, KS, ST, XF>};
+  return {BM, BN, fit(T::SMEM, T::NW), 128 * KS * std::max(ST, T::SR * T::GT), s, e, c, w, f,
+          launch_tile<BM, BN, WM, WN, KG, KS, ST, XF>};
 }
 template <int BM, int BN, int WM, int WN, int STX, int SGB, int XF>
 constexpr Shape big(float s, float e, float c, float w, float f) {
   using T = Big<BM, BN, WM, WN, STX, SGB, XF>;
-  return {BM, BN, fit(T::SMEM, T::NW), s, e, c, w, f, launch_big<BM, BN, WM, WN, STX, SGB, XF>};
+  return {BM, BN, fit(T::SMEM, T::NW), 2 * SGB * 32, s, e, c, w, f, launch_big<BM, BN, WM, WN, STX, SGB, XF>};
 }
 
 const Shape kShapes8[] = {
@@ -663,7 +665,7 @@ const Shape kShapes4[] = {
 };
 
 template <size_t N>
-void launch_best(const Shape (&shapes)[N], const MxGemmArgs &a, hipStream_t st) {
+const Shape &best_of(const Shape (&shapes)[N], const MxGemmArgs &a) {
   const Shape *best = nullptr;
   double least = 0;
   const double steps = (a.nb + 3) / 4;
@@ -676,14 +678,27 @@ void launch_best(const Shape (&shapes)[N], const MxGemmArgs &a, hipStream_t st) 
       least = t;
     }
   }
-  best->launch(a, st);
+  return *best;
 }
+
+// slabs whose grids stay far below what a launch takes
+constexpr int64_t kSlab = int64_t(1) << 18;
 
 }  // namespace
 
+int gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t xfmt, int32_t out[3]) {
+  MxGemmArgs a{};
+  a.M = (int32_t)std::min(kSlab, M);
+  a.N = (int32_t)std::min(kSlab, d);
+  a.nb = (int32_t)((k + kBlock - 1) / kBlock);
+  const Shape &s = xfmt == kFp8 ? best_of(kShapes8, a) : best_of(kShapes4, a);
+  out[0] = s.bm;
+  out[1] = s.bn;
+  out[2] = s.ring;
+  return (int)(&s - (xfmt == kFp8 ? kShapes8 : kShapes4));
+}
+
 hipError_t launch_gemm_mx(const MxGemmArgs &all, hipStream_t st) {
-  // slabs whose grids stay far below what a launch takes
-  constexpr int64_t kSlab = int64_t(1) << 18;
   for (int64_t m0 = 0; m0 < all.M; m0 += kSlab)
     for (int64_t n0 = 0; n0 < all.N; n0 += kSlab) {
       MxGemmArgs a = all;
@@ -694,8 +709,7 @@ hipError_t launch_gemm_mx(const MxGemmArgs &all, hipStream_t st) {
       a.w += n0 * a.ldw;
       a.wsc += n0 * a.ldws;
       a.y += m0 * a.ldy + n0;
-      if (a.xfmt == kFp8) launch_best(kShapes8, a, st);
-      else launch_best(kShapes4, a, st);
+      (a.xfmt == kFp8 ? best_of(kShapes8, a) : best_of(kShapes4, a)).launch(a, st);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }

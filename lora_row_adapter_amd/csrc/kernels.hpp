@@ -216,6 +216,9 @@ struct MxGemmArgs {
   int32_t tiles_m, tiles_n;
 };
 hipError_t launch_gemm_mx(const MxGemmArgs &a, hipStream_t st);
+// Index of the tile shape it takes (of the first slab); out: its rows, columns
+// and the elements of k that the longest of its LDS rings holds.
+int gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t xfmt, int32_t out[3]);
 hipError_t launch_shrink_gather(const LoraArgs &a, hipStream_t st);
 hipError_t launch_expand_gather(const LoraArgs &a, hipStream_t st);
 // A rows per stage the LDS-staged SGMV shrink takes for this launch (per

@@ -281,6 +281,12 @@ lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
   return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
+int32_t lora_test_gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t x_format, int32_t out[3]) {
+  if (x_format != LORA_MX_FP8 && x_format != LORA_MX_FP4) return -1;
+  if (out == nullptr || M < 1 || d < 1 || k < 1 || k > INT32_MAX - 512) return -1;
+  return gemm_mx_shape(M, k, d, x_format, out);
+}
+
 size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_format,
                                       int32_t n_slices, const lora_slice_t *slices) {
   if (x_format != LORA_MX_FP8 && x_format != LORA_MX_FP4) return 0;

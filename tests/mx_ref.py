@@ -87,3 +87,20 @@ def f64(t):
 def half_step(dtype):
     """Largest relative error of one rounding to nearest."""
     return torch.finfo(dtype).eps / 2
+
+
+# (M, k, d) for each of the product's tile shapes in turn, by the format of x:
+# k goes nearly twice round the longest ring of LDS tiles or scales and ends
+# inside a block; d (and M but for the smallest tiles) is whole tiles and a part.
+LONG = {
+    FP8: [
+        (1, 8204, 19), (18, 4421, 2074), (2103, 4135, 71), (34, 4418, 6539), (49, 3132, 9651), (4225, 3391, 68),
+        (102, 3042, 5705), (67, 3089, 8216), (3273, 2195, 285), (129, 2260, 8223), (539, 4043, 7444),
+        (4127, 4067, 686), (5480, 4059, 666), (1561, 2055, 3801), (775, 2321, 8363), (1036, 2072, 8909),
+        (1381, 2114, 8196)],
+    FP4: [
+        (1, 8016, 19), (33, 4241, 4174), (33, 4083, 1466), (2823, 4021, 73), (34, 4559, 6198), (5486, 3133, 66),
+        (69, 3150, 6418), (71, 2719, 8367), (3351, 3151, 263), (142, 3185, 8253), (270, 2114, 9552),
+        (5709, 4231, 264), (5545, 4003, 457), (1025, 2098, 5542), (517, 2319, 9825), (1410, 2090, 5448),
+        (1092, 2082, 8278), (1113, 2125, 9838)],
+}

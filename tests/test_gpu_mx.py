@@ -860,3 +860,11 @@ def test_profiler_times_the_product_and_the_layer():
         two = lr.Profiler.read(reset=True)
     assert one["gemm"]["launches"] == 1 and one["gemm"]["ms"] > 0
     assert two["gemm"]["launches"] == 2 and two["sgmv_shrink"]["launches"] == 1 == two["sgmv_expand"]["launches"]
+
+
+@pytest.mark.parametrize("M,k,d,fmt", [t + (f,) for f in FORMATS for t in R.LONG[f]])
+def test_product_exact_past_the_rings_of_every_tile_shape(M, k, d, fmt):
+    """k long enough that every LDS stage and scale slot is read, freed and
+    filled again (sums up to 64 k < 2^24: exact)."""
+    assert lr.test_gemm_mx_shape(M, k, d, fmt)[0] == R.LONG[fmt].index((M, k, d))
+    test_product_exact_on_whole_numbers(M, k, d, fmt)

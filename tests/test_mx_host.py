@@ -295,3 +295,26 @@ def test_layer_workspace_is_what_the_layer_checks_for(M, k, d):
         short = dict(M=M, k=k, ldx=k, fmt=fmt, W=mx(fmt=2, ldq=k // 2, lds=max(k // 32, 4), q=1 << 40, scales=1 << 41),
                      sl=sl, ldy=d, x=1 << 33, y=1 << 34, ws=1 << 45)
         assert layer(ws_bytes=n - 1, **short) == WORKSPACE
+
+
+@pytest.mark.parametrize("fmt", [R.FP8, R.FP4])
+def test_long_sizes_reach_every_tile_shape(fmt):
+    """The sizes of the products with long k take each tile shape once, go
+    round its rings and leave a part of a tile."""
+    for i, (M, k, d) in enumerate(R.LONG[fmt]):
+        at, rows, cols, ring = lr.test_gemm_mx_shape(M, k, d, fmt)
+        assert at == i
+        assert k > 1.9 * ring and k % 32 and d > cols and d % cols and M % rows
+    seen = {lr.test_gemm_mx_shape(int(2 ** m), int(2 ** k), int(2 ** d), fmt)[0]
+            for m in np.arange(0, 13.1, 0.25) for k in np.arange(5, 14, 0.5) for d in np.arange(0, 14.1, 0.25)}
+    assert seen <= set(range(len(R.LONG[fmt])))
+
+
+def test_shape_hook_refuses():
+    lib = lr.load_library()
+    out = (ctypes.c_int32 * 3)()
+    for bad in ((0, 64, 8, 1, out), (4, 0, 8, 1, out), (4, 64, 0, 1, out), (4, 64, 8, 3, out), (4, 64, 8, 1, None),
+                (4, 1 << 31, 8, 1, out)):
+        assert lib.lora_test_gemm_mx_shape(*bad) == -1
+    with pytest.raises(lr.LoraError):
+        lr.test_gemm_mx_shape(4, 64, 8, 0)
