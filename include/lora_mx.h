@@ -143,8 +143,10 @@ size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_for
  *   xn = x, or with a norm (not NULL) the normed rows of lora_rmsnorm
  *   y[m, :] = quant(xn)[m, :] dequant(W)^T + scale_s (xn[m, :] A_s^T) B_s^T
  * W: FP4, the slices' base weights stacked by rows.  x_format: the format in
- * which xn meets W (lora_mxformat_t); the adapters read xn in bf16.  With a
- * norm, residual_out receives x + residual as in lora_rmsnorm; it may be x
+ * which xn meets W (lora_mxformat_t); the adapters read xn in bf16.  The base
+ * term passes through y in bf16: rows without an adapter are rounded once,
+ * adapted ones a second time with the adapter's term added (fp32 sums; x A_s^T
+ * meets B_s^T as two bf16 parts, 16 bits).  With a norm, residual_out receives x + residual as in lora_rmsnorm; it may be x
  * or the residual itself.  y must not overlap x, the residual or residual_out,
  * nor any of the four the workspace, nor y, residual_out or the workspace W or
  * the norm's weight (LORA_ERR_ARG).  Profiling counts the norm or quantising,

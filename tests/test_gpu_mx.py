@@ -868,3 +868,41 @@ def test_product_exact_past_the_rings_of_every_tile_shape(M, k, d, fmt):
     filled again (sums up to 64 k < 2^24: exact)."""
     assert lr.test_gemm_mx_shape(M, k, d, fmt)[0] == R.LONG[fmt].index((M, k, d))
     test_product_exact_on_whole_numbers(M, k, d, fmt)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("with_norm", [False, True])
+@pytest.mark.parametrize("M,k,d,scale", [(1, 256, 96, 1.0), (37, 264, 200, 1.0), (300, 1024, 288, 0.03),
+                                         (530, 512, 1000, 30.0), (700, 2048, 264, 1.0)])
+def test_layer_roundings(M, k, d, scale, with_norm, fmt):
+    """Every element within its two roundings: h = 2^-8 of the base term (in
+    bf16 on its way through y) and h of the sum, with the sums' own error E on
+    top.  E: fp32 sums over k <= 2^11 of the base and of x A^T (2^-23 an
+    addition, 2^-12 of the magnitudes' sum), the two bf16 parts of x A^T (2^-16)
+    and the sum over the rank (64 x 2^-23): 2^-11 of the magnitudes' sums at
+    most.  Rows without an adapter are rounded once."""
+    w = wl.custom(seed=M + 1, M=M, k=k, d=d, ranks=[4, 16, 64, 8], max_rank=64, none_frac=0.2)
+    w.scales = (w.scales * scale).astype(np.float32)
+    slices, W, Wv = layer_inputs(w)
+    x, ids = w.x.cuda(), torch.from_numpy(w.ids).cuda()
+    norm, X, xn = None, R.f64(w.x), R.f64(w.x)
+    if with_norm:
+        g = (1 + 0.2 * torch.randn(k, generator=torch.Generator().manual_seed(1))).to(BF)
+        norm = lr.Norm(g.cuda(), 1e-5)
+        X = R.rmsnorm(X, R.f64(g), 1e-5)[1]
+        xn = R.f64(lr.lora_rmsnorm(x, norm))  # its own test compares it with X
+    XQ, p = R.quantised_values(X, fmt), w.proj("out")
+    base, mag = XQ @ Wv.T, np.abs(XQ) @ np.abs(Wv).T
+    delta, dmag = np.zeros((M, d)), np.zeros((M, d))
+    for s in range(w.S):
+        m, A, Bm, sc = w.ids == s, R.f64(p.A[s]), R.f64(p.B[s]), float(w.scales[s])
+        delta[m] = sc * (xn[m] @ A.T @ Bm.T)
+        dmag[m] = abs(sc) * (np.abs(xn[m]) @ np.abs(A).T @ np.abs(Bm).T)
+    h, want, E = R.half_step(BF), base + delta, 2.0 ** -12 * mag + 2.0 ** -11 * dmag
+    once = h * (np.abs(base) + E)
+    limit = np.where((w.ids >= 0)[:, None], once + h * (np.abs(want) + E + once), once) + E
+    for path in (lr.PATH_AUTO, lr.PATH_GATHER, lr.PATH_SGMV):
+        err = np.abs(R.f64(lr.lora_linear_sliced_mx(x, W, slices, ids, x_format=fmt, norm=norm, path=path)) - want)
+        say("layer %dx%dx%d norm %s fmt %d path %d: %.3f of the limit" % (M, k, d, with_norm, fmt, path,
+                                                                         (err / limit).max()))
+        assert (err <= limit).all()
