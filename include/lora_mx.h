@@ -33,7 +33,8 @@
  *
  * Conventions as in lora_row.h: device pointers, row-major, asynchronous on
  * `stream`, errors as lora_status_t, no device allocation, safe to capture
- * into a graph.  M == 0 is a no-op.  Row counts, k and d are at most 2^31 - 1.
+ * into a graph.  M == 0 is a no-op.  Row counts, k and d are at most 2^31 - 1,
+ * strides 2^40 bytes, where an operator sets no other limit.
  * lora_profile_* times the product (LORA_K_GEMM) and the layer; quantising,
  * reading back and the norm called by themselves have no class and are not
  * timed.
@@ -115,7 +116,10 @@ lora_status_t lora_rmsnorm(lora_dtype_t dtype, int64_t M, int64_t k, const void 
  * (LORA_ERR_UNSUPPORTED otherwise), y [M, d] bf16 (ldy >= d).  Products and
  * sums run in the scaled matrix instructions with fp32 accumulators; y is
  * rounded once.  Deterministic: the summation order depends on the shape only.
- * y must not overlap an operand (LORA_ERR_ARG).
+ * Two scales multiply without a range of their own; sums that leave fp32's on
+ * the way become infinities or NaNs, as fp32 additions do.  y must not overlap an
+ * operand (LORA_ERR_ARG).  ldq and lds of both operands are at most 2^23, so k
+ * is at most 2^23 where x is FP8 and 2^24 where it is FP4 (LORA_ERR_SHAPE).
  */
 lora_status_t lora_gemm_mx(int64_t M, int64_t k, int64_t d, const lora_mx_t *x,
                            const lora_mx_t *W, void *y, int64_t ldy, void *stream);
@@ -145,15 +149,16 @@ size_t lora_workspace_bytes_sliced_mx(int64_t max_rows, int64_t k, int32_t x_for
  * W: FP4, the slices' base weights stacked by rows.  x_format: the format in
  * which xn meets W (lora_mxformat_t); the adapters read xn in bf16.  The base
  * term passes through y in bf16: rows without an adapter are rounded once,
- * adapted ones a second time with the adapter's term added (fp32 sums; x A_s^T
- * meets B_s^T as two bf16 parts, 16 bits).  With a norm, residual_out receives x + residual as in lora_rmsnorm; it may be x
- * or the residual itself.  y must not overlap x, the residual or residual_out,
- * nor any of the four the workspace, nor y, residual_out or the workspace W or
- * the norm's weight (LORA_ERR_ARG).  Profiling counts the norm or quantising,
- * and the plan beside it, with the product (LORA_K_GEMM).
- * Everything else as in lora_linear_sliced (k, ldx multiples of 8, x 16-byte
- * aligned; lora_check reports on the workspace; up to LORA_PLAN_MAX_ROWS rows
- * those with no adapter equal lora_gemm_mx of the quantised rows bitwise).
+ * adapted ones a second time with the adapter's term added (fp32 sums; xn
+ * A_s^T keeps 16 bits or more).  With a norm, residual_out receives x +
+ * residual as in lora_rmsnorm; it may be x or the residual itself.  y must not
+ * overlap x, the residual or residual_out, nor any of the four the workspace,
+ * nor y, residual_out or the workspace W or the norm's weight (LORA_ERR_ARG).
+ * Profiling counts the norm or quantising, and the plan beside it, with the
+ * product (LORA_K_GEMM).  Everything else as in lora_linear_sliced (k <= 2^23,
+ * k, ldx multiples of 8, x 16-byte aligned; lora_check reports on the
+ * workspace; up to LORA_PLAN_MAX_ROWS rows those with no adapter equal
+ * lora_gemm_mx of the quantised rows bitwise).
  */
 lora_status_t lora_linear_sliced_mx(int64_t M, int64_t k, const void *x, int64_t ldx,
                                     const lora_norm_t *norm, int32_t x_format, const lora_mx_t *W,

@@ -373,10 +373,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_gemm_mx_tile(MxGemmArgs p
 }
 
 // ---------------------------------------------------------------------------
-// Large tiles: every load a run of 128 bytes of a row.  What a load into LDS
-// costs is its number of 128-byte lines (2.2 cycles of a CU each, measured;
-// half a line costs as much), and that bounds a CU's feed: hence W's pairs of
-// steps also where x goes by steps.
+// Large tiles: every load a run of 128 bytes of a row, and so W's pairs of
+// steps also where x goes by steps: a load into LDS costs a CU 2.2 cycles a
+// 128-byte line (measured; half a line costs as much).  At 8192 x 9216 x 8192
+// fp4 that is 90 of the 280 us that the loads alone take; the rest is their
+// wait for the L2s' answers, with one pair of tiles on its way (10 TB/s).
 // ---------------------------------------------------------------------------
 
 // k runs in pairs of steps (256 elements).  W's ring holds two pairs, x's STX
@@ -601,9 +602,14 @@ void launch_tile(MxGemmArgs a, hipStream_t st) {
 // M from 1 to 8192, d x k of 9216 x 8192, 4096 x 4096, 5120 x 5120, 2048 x
 // 4096, 1024 x 1024, 1024 x 8192, 9216 x 512 and 8192 x 1024), good to 2 - 8%;
 // the choice is within 1% of the best of 37 shapes tried, on the mean.  Of
-// those the table holds the ones without which that gets worse.  128 x 9216 x
-// 8192 fp8 takes 20.1 us (64 x 128 tiles 25), 256 x 9216 x 8192 28.6 (128 x
-// 144 tiles 41), 512 x 5120 x 5120 20.3 (28).
+// those the table holds the ones without which that gets worse: by the model,
+// leaving one out costs 0.06 to 4% on the mean of the fitted sizes (fp4's 64 x
+// 96 tiles 0.006%, its large 64 x 128 ones nothing there) and 0.02 to 6% over
+// M from 1 to 8192, k and d from 64 to 8192 and 9216, uniform in the logarithm.
+// Over those the least used are fp4's 192 x 128 tiles (4 of 20000 sizes,
+// 0.002%; 0.06% of the fitted ones) and fp8's 32 x 80 (13, 0.006%; 0.08%).
+// 128 x 9216 x 8192 fp8 takes 20.1 us (64 x 128 tiles 25), 256 x 9216 x 8192
+// 28.6 (128 x 144 tiles 41), 512 x 5120 x 5120 20.3 (28).
 struct Shape {
   int bm, bn, fit;
   int ring;  // elements of k that the longest LDS ring holds

@@ -906,3 +906,24 @@ def test_layer_roundings(M, k, d, scale, with_norm, fmt):
         say("layer %dx%dx%d norm %s fmt %d path %d: %.3f of the limit" % (M, k, d, with_norm, fmt, path,
                                                                          (err / limit).max()))
         assert (err <= limit).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("M,k,d", [(3, 256, 40), (300, 2080, 520)])
+def test_product_at_far_scales(M, k, d, fmt):
+    """Scales at both ends whose products are ordinary, subnormal or nothing,
+    and the largest two over zero codes: whole numbers times one power of two,
+    so exact but for the last rounding."""
+    g = np.random.default_rng(k)
+    vals = R.code_values(fmt)
+    cx = np.flatnonzero(np.isfinite(vals) & (np.abs(vals) <= 4) & (vals == np.round(vals))).astype(np.uint8)
+    cw = np.array([2, 4, 5, 6, 10, 12, 13, 14], np.uint8)  # 1, 2, 3, 4 and their negatives
+    nb = -(-k // 32)
+    for sx, sw in ((254, 0), (0, 254), (127, 0), (0, 127), (60, 60), (100, 20), (40, 70), (0, 0), (254, 254)):
+        x, w = cx[g.integers(0, cx.size, (M, nb * 32))], cw[g.integers(0, cw.size, (d, nb * 32))]
+        SX, SW = np.full((M, nb), sx, np.uint8), np.full((d, nb), sw, np.uint8)
+        if sx + sw == 508:  # only the first block counts
+            x[:, 32:], SX[:, 0], SW[:, 0] = 0, 127, 127
+        y = lr.lora_gemm_mx(to_device(x, SX, fmt, k), to_device(w, SW, R.FP4, k)).cpu()
+        want = R.dequantise(x, SX, fmt, k) @ R.dequantise(w, SW, R.FP4, k).T
+        assert torch.equal(y, torch.from_numpy(want).float().to(BF)), (sx, sw)
