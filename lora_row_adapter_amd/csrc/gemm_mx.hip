@@ -383,8 +383,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_gemm_mx_tile(MxGemmArgs p
 // k runs in pairs of steps (256 elements).  W's ring holds two pairs, x's STX
 // tiles of 128 bytes a row: a pair in fp4, a step in fp8; scales SGB bytes a
 // row (SGB / 8 pairs), two groups.
-// 8192 x 9216 x 8192: fp4 335 us (3.7 PFLOP/s; a loop of the products on
-// registers reaches 7.1), fp8 520 (2.4; 4.8); 512 x 9216 x 8192 fp8 41 us.
+// 8192 x 9216 x 8192: fp4 340 us (3.6 PFLOP/s; a loop of the products on
+// registers reaches 7.1), fp8 466 (2.7; 4.8); 512 x 9216 x 8192 fp8 43 us
+// (three sets of inputs or more in turn; with one, 310, 450 and 39).
 // Without the loads into LDS they take 268, 400 and 32, the loads alone 280,
 // 310 and 29: bound by neither alone, but by how far the two overlap.
 template <int BM, int BN, int WM, int WN, int STX, int SGB, int XF>

@@ -161,7 +161,7 @@ __device__ __forceinline__ double row_sum(double s, int log_tpr, double *red) {
 // The squares are summed in 64 bits (a conversion and an addition per input
 // cost about what the memory takes anyway).  The outputs are those of one
 // rounding of the 64-bit y, but computing them in 64 bits throughout costs
-// 143 us, not 110, at 8192 x 8192 bf16 with a residual (604 MB, 5.5 TB/s):
+// 143 us, not 113, at 8192 x 8192 bf16 with a residual (604 MB, 5.3 TB/s):
 // they are computed in fp32 and redone in 64 bits where the two could differ.
 // NC > 0: each thread keeps its NC chunks of x and the residual in registers,
 // so every input is read once; NC == 0: rows too long for that are read twice.
