@@ -927,3 +927,94 @@ def test_product_at_far_scales(M, k, d, fmt):
         y = lr.lora_gemm_mx(to_device(x, SX, fmt, k), to_device(w, SW, R.FP4, k)).cpu()
         want = R.dequantise(x, SX, fmt, k) @ R.dequantise(w, SW, R.FP4, k).T
         assert torch.equal(y, torch.from_numpy(want).float().to(BF)), (sx, sw)
+
+
+# ------------------------------------------------------------ calls that the documents allow
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_product_of_more_columns_than_a_slab(fmt):
+    """More than 2^18 rows of W: launches of their own for those past them."""
+    d = (1 << 18) + 700
+    x, X = whole_mx(1, 3, 96, fmt)
+    W, Wv = whole_mx(2, d, 96, lr.MX_FP4)
+    assert same_bits(lr.lora_gemm_mx(x, W).cpu(), torch.from_numpy(X @ Wv.T).float().to(BF))
+
+
+def rows_in_wide(t, before, after, fill=5.0):
+    """The same rows as columns of a wider tensor."""
+    wide = torch.full((t.shape[0], before + t.shape[1] + after), fill, dtype=t.dtype, device="cuda")
+    v = wide[:, before:before + t.shape[1]]
+    v.copy_(t)
+    return wide, v
+
+
+@pytest.mark.parametrize("path", [lr.PATH_AUTO, lr.PATH_GATHER, lr.PATH_SGMV])
+@pytest.mark.parametrize("with_norm", [False, True])
+@pytest.mark.parametrize("M,k,d", [(1, 64, 33), (130, 264, 201), (700, 512, 1)])
+def test_layer_of_odd_widths_in_wider_tensors(M, k, d, with_norm, path):
+    """Every tensor a column range of a wider one, y and the norm's at odd
+    offsets: the bits of the same rows alone, and nothing beside them."""
+    w = wl.custom(seed=d, M=M, k=k, d=d, ranks=[4, 16, 64, 8], max_rank=64, none_frac=0.2)
+    slices, W, _ = layer_inputs(w)
+    x, ids = w.x.cuda(), torch.from_numpy(w.ids).cuda()
+    res, g = rand(3, M, k, BF).cuda(), torch.ones(k, dtype=BF, device="cuda")
+    h = torch.empty_like(x) if with_norm else None
+    want = lr.lora_linear_sliced_mx(x, W, slices, ids, path=path, norm=lr.Norm(g, 1e-5, res, h) if with_norm else None)
+    Xw, xs = rows_in_wide(x, 8, 16)
+    Rw, rs = rows_in_wide(res, 3, 2)
+    Hw, hs = rows_in_wide(torch.zeros_like(res), 1, 4)
+    Yw, ys = rows_in_wide(torch.zeros(M, d, dtype=BF, device="cuda"), 3, 7)
+    norm = lr.Norm(g, 1e-5, rs, hs) if with_norm else None
+    lr.lora_linear_sliced_mx(xs, W, slices, ids, path=path, norm=norm, y=ys)
+    assert torch.equal(ys, want)
+    assert (Yw[:, :3] == 5).all() and (Yw[:, 3 + d:] == 5).all()
+    assert (Xw[:, :8] == 5).all() and (Xw[:, 8 + k:] == 5).all() and torch.equal(xs, x)
+    if with_norm:
+        assert torch.equal(hs, h) and (Hw[:, :1] == 5).all() and (Hw[:, 1 + k:] == 5).all()
+
+
+def test_layer_of_ranks_past_the_matrix_paths(oracle_mod):
+    """Ranks up to 128 take the gather path; SGMV refuses them."""
+    w = wl.custom(seed=2, M=90, k=256, d=136, ranks=[128, 8, 100], max_rank=128, none_frac=0.1)
+    slices, W, Wv = layer_inputs(w)
+    x, ids = w.x.cuda(), torch.from_numpy(w.ids).cuda()
+    want = oracle_layer(oracle_mod, w, ["out"], w.x, R.quantised_values(R.f64(w.x), R.FP8), Wv)
+    assert normwise(R.f64(lr.lora_linear_sliced_mx(x, W, slices, ids)), want) <= TOL
+    with pytest.raises(lr.LoraError):
+        lr.lora_linear_sliced_mx(x, W, slices, ids, path=lr.PATH_SGMV)
+
+
+def test_layer_captured_with_a_plan_of_its_own():
+    """More than 64 adapters: the plan runs on a stream beside, in a graph as
+    outside; two captured layers replayed in turn with eager ones between."""
+    w = wl.custom(seed=13, M=64, k=512, d=320, ranks=[8, 32], max_rank=32, none_frac=0.2)
+    slices, W, _ = layer_inputs(w)
+    slices = more_slots(slices, 80)
+    g = torch.ones(512, dtype=BF, device="cuda")
+    n = lr.workspace_bytes_sliced_mx(64, 512, lr.MX_FP8, slices)
+    sets = [(rand(i, 64, 512, BF).cuda(), torch.from_numpy(np.roll(w.ids, i)).cuda(),
+             torch.empty(n, dtype=torch.uint8, device="cuda"), torch.empty(64, 320, dtype=BF, device="cuda"))
+            for i in range(2)]
+
+    def call(i):
+        x, ids, ws, y = sets[i]
+        return lr.lora_linear_sliced_mx(x, W, slices, ids, norm=lr.Norm(g), y=y, workspace=ws)
+
+    for i in (0, 1):
+        call(i)
+    torch.cuda.synchronize()
+    graphs = []
+    for i in (0, 1):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            call(i)
+    for rep in range(4):
+        for i in (0, 1):
+            sets[i][0].copy_(rand(60 + 2 * rep + i, 64, 512, BF))
+            sets[i][3].zero_()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for i in (0, 1):
+            got = sets[i][3].clone()
+            want = lr.lora_linear_sliced_mx(sets[i][0], W, slices, sets[i][1], norm=lr.Norm(g))
+            assert torch.equal(got, want)
