@@ -1,0 +1,121 @@
+/*
+ * lora_w4.h -- a 4-bit base weight with group scales and zero points for the
+ * multi-adapter LoRA linear layer (C ABI, part of liblora_row.so): laying the
+ * weight out, reading it back, the base product from one row to long prompts,
+ * and the layer on top of it.
+ *
+ * "Your LoRA Adapters Are Thrashing Your GPUs", section 02: production
+ * deployments quantize the base model to INT4 and keep the LoRA weights in 16
+ * bits.  lora_qweight_t (lora_row.h) is the symmetric form in checkpoint
+ * order, for batches; here the codes have a zero point, groups are as small as
+ * 32 and need not divide k, and the weight is laid out once, so that one
+ * token's product runs at the rate of its bytes.
+ *
+ * Weight: codes q[n, j] in 0 .. 15; columns j with the same j / group share a
+ * scale and a zero point z (a whole number, 0 .. 31):
+ *   W[n, j] = scale[n, j / group] (q[n, j] - z[n, j / group])
+ * The last group of a row is shorter where `group` does not divide k.
+ * group: 32, 64 or a multiple of 128.
+ *
+ * Conventions as in lora_row.h: device pointers, row-major, asynchronous on
+ * `stream`, errors as lora_status_t, no device allocation, safe to capture
+ * into a graph.  M == 0 is a no-op.  M, k and d are at most 2^31 - 1 (k here
+ * at most 2^24), strides 2^40 bytes.  Products and layers are timed by
+ * lora_profile_* (LORA_K_GEMM; the layer's steps under their own classes).
+ */
+#ifndef LORA_W4_H
+#define LORA_W4_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "lora_row.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* A weight [d, k] as lora_w4_pack lays it out.  The struct is HOST memory,
+ * read during the call only. */
+typedef struct lora_w4 {
+  int32_t group;
+  const void *data; /* device, 256-byte aligned, lora_w4_bytes(d, k, group) */
+} lora_w4_t;
+
+/* Bytes of a laid-out weight: 4.25 bits a weight (group >= 128; 4.5 with 64, 5
+ * with 32), d rounded up to 16 and k to 128.  Host-only; 0 on invalid
+ * arguments. */
+size_t lora_w4_bytes(int64_t d, int64_t k, int32_t group);
+
+/*
+ * Lay out a checkpoint's weight.
+ *   q: uint8 [d, ldq], two codes to a byte, column 2i in the low nibble of
+ *      byte i; ldq >= ceil(k / 2);
+ *   scales: [d, lds] of scale_dtype (F32 or BF16), lds >= ceil(k / group);
+ *   zeros: uint8 [d, ldz], ldz >= ceil(k / group), or NULL (8 throughout);
+ *      bytes are taken modulo 32.
+ * Each scale is kept with 19 significant bits: exact for scales that were
+ * bf16 or fp16 before, else rounded to nearest (2^-19 relative).  A NaN or an
+ * infinity stays one.  Any alignment of q and zeros.  out must not overlap
+ * the others (LORA_ERR_ARG).
+ */
+lora_status_t lora_w4_pack(int64_t d, int64_t k, int32_t group, const uint8_t *q, int64_t ldq,
+                           lora_dtype_t scale_dtype, const void *scales, int64_t lds,
+                           const uint8_t *zeros, int64_t ldz, void *out, void *stream);
+
+/*
+ * y = W (with the scales as kept), rounded once to F32 or BF16; y [d, k],
+ * ldy >= k, any alignment of its elements' size; must not overlap W.
+ */
+lora_status_t lora_w4_dequantize(lora_dtype_t dtype, int64_t d, int64_t k, const lora_w4_t *W,
+                                 void *y, int64_t ldy, void *stream);
+
+/*
+ * Bytes of workspace with which lora_gemm_w4 is fastest for this size (0:
+ * none; never more than 256 MiB and that of lora_gemm).  Host-only.
+ */
+size_t lora_gemm_w4_workspace_bytes(int64_t M, int64_t k, int64_t d);
+
+/*
+ * y = x W^T: x bf16 [M, k] (k, ldx multiples of 8, 16-byte aligned), y bf16
+ * [M, d] (ldy >= d).  Codes meet x exactly; each group's sum is scaled and
+ * added in fp32, y rounded once.  Where a workspace of
+ * lora_gemm_w4_workspace_bytes(M, k, d) bytes (256-byte aligned, no
+ * initialisation) is given and that is not 0, the weight is read back into it
+ * as bf16, each weight rounded once, and multiplied as lora_gemm does; smaller
+ * or NULL: the first form.  Sums that leave fp32's range on the way (|x| past
+ * 2^120 or so) and infinities in x may become NaN in their row.
+ * Deterministic: the summation order depends on the sizes alone (and on
+ * whether there is a workspace).  y must not overlap x, W or the workspace
+ * (LORA_ERR_ARG).
+ */
+lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                           const lora_w4_t *W, void *y, int64_t ldy, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
+/*
+ * Bytes of workspace lora_linear_sliced_w4 needs for up to max_rows rows (any
+ * path).  Host-only; 0 on invalid arguments.  256-byte aligned, caller-owned,
+ * no initialisation needed (but zero-fill it once where lora_check's
+ * n_sync_expired is read).
+ */
+size_t lora_workspace_bytes_sliced_w4(int64_t max_rows, int64_t k, int32_t n_slices,
+                                      const lora_slice_t *slices);
+
+/*
+ * lora_linear_sliced over such a base weight (bf16 x, y, adapters): W stacks
+ * the slices' base weights by rows.  Everything else as in
+ * lora_linear_sliced.  y must not overlap x, W or the workspace
+ * (LORA_ERR_ARG).
+ */
+lora_status_t lora_linear_sliced_w4(int64_t M, int64_t k, const void *x, int64_t ldx,
+                                    const lora_w4_t *W, int32_t n_slices,
+                                    const lora_slice_t *slices, const int32_t *adapter_ids, void *y,
+                                    int64_t ldy, void *workspace, size_t workspace_bytes,
+                                    int32_t path, uint32_t flags, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* LORA_W4_H */

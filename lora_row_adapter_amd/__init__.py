@@ -1,8 +1,8 @@
 """Multi-adapter LoRA linear layer for AMD MI355X (gfx950).
 
 The product is the C-ABI library ``liblora_row.so`` (HIP kernels for CDNA4),
-declared in ``include/lora_row.h``, ``include/lora_pool.h`` and
-``include/lora_mx.h``; this package is a thin ctypes binding
+declared in ``include/lora_row.h``, ``include/lora_pool.h``, ``include/lora_mx.h``,
+``include/lora_w4.h`` and ``include/lora_heads.h``; this package is a thin ctypes binding
 with the same entry-point names.  The library is loaded on first use and its
 absence is an error: there is no fallback.
 """
@@ -14,4 +14,6 @@ from ._binding import (  # noqa: F401
     status_str, workspace_bytes, workspace_bytes_sliced, gemm_workspace_bytes, test_sync_spin_limit,
     MX, MX_FP4, MX_FP8, Norm, test_gemm_mx_shape, lora_gemm_mx, lora_linear_sliced_mx, lora_mx_dequantize,
     lora_mx_quantize, lora_rmsnorm, workspace_bytes_sliced_mx,
+    W4, gemm_w4_workspace_bytes, lora_gemm_w4, lora_linear_sliced_w4, lora_w4_dequantize, lora_w4_pack,
+    workspace_bytes_sliced_w4, Rope, lora_qk_norm_rope,
 )

@@ -107,6 +107,36 @@ class _CNorm(ctypes.Structure):
     ]
 
 
+class _CW4(ctypes.Structure):
+    _fields_ = [
+        ("group", ctypes.c_int32),
+        ("data", ctypes.c_void_p),
+    ]
+
+
+class _CHeads(ctypes.Structure):
+    _fields_ = [
+        ("n_heads", ctypes.c_int32),
+        ("x", ctypes.c_void_p),
+        ("ld_row", ctypes.c_int64),
+        ("ld_head", ctypes.c_int64),
+        ("weight", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("ldo_row", ctypes.c_int64),
+        ("ldo_head", ctypes.c_int64),
+    ]
+
+
+class _CRope(ctypes.Structure):
+    _fields_ = [
+        ("positions", ctypes.c_void_p),
+        ("inv_freq", ctypes.c_void_p),
+        ("rot_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class _CPoolDesc(ctypes.Structure):
     _fields_ = [
         ("pool", ctypes.c_void_p),
@@ -200,6 +230,24 @@ def load_library():
     lib.lora_linear_sliced_mx.argtypes = [i64, i64, p, i64, pno, i32, pmx, i32, psl, p, p, i64, p,
                                           sz, i32, u32, p]
     lib.lora_linear_sliced_mx.restype = i32
+    pw4 = ctypes.POINTER(_CW4)
+    lib.lora_w4_bytes.argtypes = [i64, i64, i32]
+    lib.lora_w4_bytes.restype = sz
+    lib.lora_w4_pack.argtypes = [i64, i64, i32, p, i64, i32, p, i64, p, i64, p, p]
+    lib.lora_w4_pack.restype = i32
+    lib.lora_w4_dequantize.argtypes = [i32, i64, i64, pw4, p, i64, p]
+    lib.lora_w4_dequantize.restype = i32
+    lib.lora_gemm_w4_workspace_bytes.argtypes = [i64, i64, i64]
+    lib.lora_gemm_w4_workspace_bytes.restype = sz
+    lib.lora_gemm_w4.argtypes = [i64, i64, i64, p, i64, pw4, p, i64, p, sz, p]
+    lib.lora_gemm_w4.restype = i32
+    lib.lora_workspace_bytes_sliced_w4.argtypes = [i64, i64, i32, psl]
+    lib.lora_workspace_bytes_sliced_w4.restype = sz
+    lib.lora_linear_sliced_w4.argtypes = [i64, i64, p, i64, pw4, i32, psl, p, p, i64, p, sz, i32, u32, p]
+    lib.lora_linear_sliced_w4.restype = i32
+    phd = ctypes.POINTER(_CHeads)
+    lib.lora_qk_norm_rope.argtypes = [i32, i64, i32, ctypes.c_float, phd, phd, ctypes.POINTER(_CRope), p]
+    lib.lora_qk_norm_rope.restype = i32
     lib.lora_merge.argtypes = [i32, i64, i64, p, i64, pad, i32, p, ctypes.c_float, p, i64, p]
     lib.lora_merge.restype = i32
     lib.lora_translate.argtypes = [pad, p, p, i64, p, p]
@@ -1047,6 +1095,263 @@ def lora_linear_sliced_mx(x: torch.Tensor, W: MX, slices, adapter_ids: torch.Ten
         len(slices), _slice_array(slices), _dev(adapter_ids, "adapter_ids", torch.int32), yp, ldy,
         _dev(workspace, "workspace"), workspace.numel(), int(path), int(flags))
     return y
+
+
+def _same_device(t: torch.Tensor, name: str, device) -> None:
+    if t.device != device:
+        raise ValueError("%s must be a tensor on %s" % (name, device))
+
+
+def _check_layer(slices, adapter_ids: torch.Tensor, M: int, k: int, dtype, device) -> None:
+    """What the C call cannot see of a layer's adapters: element counts,
+    types and devices."""
+    if adapter_ids.numel() != M:
+        raise ValueError("adapter_ids must have one entry per row")
+    _same_device(adapter_ids, "adapter_ids", device)
+    for sl in slices:
+        ad = sl.adapters
+        _same_device(ad.ranks, "the adapters' ranks", device)
+        _same_device(sl.scales, "scales", device)
+        if sl.scales.numel() < ad.n_adapters:
+            raise ValueError("scales must have one entry per adapter")
+        if ad.kind == KIND_SLOTS:
+            if ad.A.dtype is not dtype:
+                raise TypeError("adapter slots must have x's dtype")
+            if ad.A.shape[0] != ad.n_adapters or ad.A.shape[2] != k or ad.B.shape[1] != sl.d:
+                raise ValueError("adapter slots must be A [S, R, %d] and B [S, %d, R]" % (k, sl.d))
+
+
+class W4:
+    """A 4-bit weight [d, k] with group scales and zero points as
+    lora_w4_pack lays it out (include/lora_w4.h); `data`: uint8, device."""
+
+    __slots__ = ("d", "k", "group", "data", "device", "_c", "_ref")
+
+    def __init__(self, d: int, k: int, group: int, data: torch.Tensor):
+        self.d, self.k, self.group = int(d), int(k), int(group)
+        if data.dtype is not torch.uint8 or not data.is_cuda or not data.is_contiguous():
+            raise TypeError("data must be a contiguous uint8 device tensor")
+        if data.numel() < self.bytes(d, k, group):
+            raise ValueError("data is shorter than the weight")
+        self.data, self.device = data, data.device
+        self._c = _CW4(self.group, data.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+    @staticmethod
+    def bytes(d: int, k: int, group: int) -> int:
+        n = int(load_library().lora_w4_bytes(int(d), int(k), int(group)))
+        if n == 0:
+            raise LoraError(2, "lora_w4_bytes")
+        return n
+
+    def ref(self):
+        return self._ref
+
+
+def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, k: int, group: int,
+                 zeros: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                 stream=None) -> W4:
+    """Lay out a checkpoint's 4-bit weight: q uint8 [d, >= ceil(k / 2)] (two
+    codes a byte, the even column low), scales float32 or bfloat16 and zeros
+    uint8 (None: 8 throughout) [d, >= ceil(k / group)].  out: the storage,
+    uint8 [W4.bytes(d, k, group)]."""
+    lib = _lib or load_library()
+    k, group = int(k), int(group)
+    device = q.device
+    if q.dtype is not torch.uint8 or q.dim() != 2 or not q.is_cuda:
+        raise TypeError("q must be a 2-D uint8 device tensor")
+    d = q.shape[0]
+    n = W4.bytes(d, k, group)
+    ng = -(-k // group)
+    dt = _DTYPES.get(scales.dtype)
+    if dt is None:
+        raise TypeError("scales must be float32 or bfloat16")
+    if zeros is not None and zeros.dtype is not torch.uint8:
+        raise TypeError("zeros must be uint8")
+
+    def lead(t, name, width):
+        if t.dim() != 2 or t.shape[0] != d or t.shape[1] < width:
+            raise ValueError("%s must be [%d, >= %d]" % (name, d, width))
+        _same_device(t, name, device)
+        ld, unit = t.stride()
+        if unit != 1 and width > 1:
+            raise ValueError("%s must have unit stride along its last dimension" % name)
+        return t.data_ptr(), ld if d > 1 else width
+
+    qp, ldq = lead(q, "q", (k + 1) // 2)
+    sp, lds = lead(scales, "scales", ng)
+    zp, ldz = (None, 0) if zeros is None else lead(zeros, "zeros", ng)
+    if out is None:
+        out = _empty(n, torch.uint8, device, stream)
+    w = W4(d, k, group, out)
+    _same_device(out, "out", device)
+    _on(device, stream, lib.lora_w4_pack, "lora_w4_pack", d, k, group, qp, ldq, dt, sp, lds, zp, ldz,
+        out.data_ptr())
+    return w
+
+
+def lora_w4_dequantize(W: W4, dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """The values W stands for (float32 or bfloat16 [d, k])."""
+    lib = _lib or load_library()
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    if out is None:
+        out = _empty((W.d, W.k), dtype, W.device, stream)
+    yp, ldy = _matrix(out, "out", (W.d, W.k), dtype, W.device)
+    _on(W.device, stream, lib.lora_w4_dequantize, "lora_w4_dequantize", dt, W.d, W.k, W._ref, yp, ldy)
+    return out
+
+
+def gemm_w4_workspace_bytes(M: int, k: int, d: int) -> int:
+    """Workspace bytes with which lora_gemm_w4 is fastest (0: none)."""
+    return int(load_library().lora_gemm_w4_workspace_bytes(int(M), int(k), int(d)))
+
+
+def lora_gemm_w4(x: torch.Tensor, W: W4, y: Optional[torch.Tensor] = None,
+                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y = x W^T (bfloat16 x [M, k] and y [M, d]).  Without a workspace one of
+    gemm_w4_workspace_bytes bytes is allocated (torch) for the call."""
+    lib = _lib or load_library()
+    bf = torch.bfloat16
+    if x.dtype is not bf:
+        raise TypeError("x must be bfloat16")
+    _, shape, device, xp, ldx = _input(x)
+    M, k = shape
+    if W.k != k or W.device != device:
+        raise ValueError("x and W differ in k or device")
+    if y is None:
+        y = _empty((M, W.d), bf, device, stream)
+        yp, ldy = y.data_ptr(), W.d
+    else:
+        yp, ldy = _matrix(y, "y", (M, W.d), bf, device)
+    if workspace is None:
+        n = lib.lora_gemm_w4_workspace_bytes(M, k, W.d)
+        if n > 0:
+            workspace = _empty(n, torch.uint8, device, stream)
+    else:
+        _same_device(workspace, "workspace", device)
+    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace", torch.uint8), workspace.numel())
+    _on(device, stream, lib.lora_gemm_w4, "lora_gemm_w4", M, k, W.d, xp, ldx, W._ref, yp, ldy, wp, wn)
+    return y
+
+
+def workspace_bytes_sliced_w4(max_rows: int, k: int, slices) -> int:
+    arr = _slice_array(slices)
+    n = load_library().lora_workspace_bytes_sliced_w4(int(max_rows), int(k), len(slices), arr)
+    if n == 0:
+        raise LoraError(1, "lora_workspace_bytes_sliced_w4")
+    return int(n)
+
+
+def lora_linear_sliced_w4(x: torch.Tensor, W: W4, slices, adapter_ids: torch.Tensor,
+                          y: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                          path: int = PATH_AUTO, flags: int = 0, stream=None) -> torch.Tensor:
+    """lora_linear_sliced over a 4-bit stacked base weight with group scales
+    and zero points (bfloat16)."""
+    lib = _lib or load_library()
+    bf = torch.bfloat16
+    if x.dtype is not bf:
+        raise TypeError("x must be bfloat16")
+    _, shape, device, xp, ldx = _input(x)
+    M, k = shape
+    d_total = sum(sl.d for sl in slices)
+    if W.d != d_total or W.k != k or W.device != device:
+        raise ValueError("W must stack the slices' weights on x's device: [%d, %d] expected" % (d_total, k))
+    _check_layer(slices, adapter_ids, M, k, bf, device)
+    if y is None:
+        y = _empty((M, d_total), bf, device, stream)
+    yp, ldy = _matrix(y, "y", (M, d_total), bf, device)
+    arr = _slice_array(slices)
+    if workspace is None:  # needs no initialisation, and lora_check sees it no more
+        n = lib.lora_workspace_bytes_sliced_w4(M, k, len(slices), arr)
+        if n == 0:
+            raise LoraError(1, "lora_workspace_bytes_sliced_w4")
+        workspace = _empty(n, torch.uint8, device, stream)
+    else:
+        _same_device(workspace, "workspace", device)
+    _on(device, stream, lib.lora_linear_sliced_w4, "lora_linear_sliced_w4", M, k, xp, ldx, W._ref,
+        len(slices), arr, _dev(adapter_ids, "adapter_ids", torch.int32), yp, ldy,
+        _dev(workspace, "workspace", torch.uint8), workspace.numel(), int(path), int(flags))
+    return y
+
+
+class Rope:
+    """A rotation by position (lora_rope_t): frequencies float32 [rot_dim / 2]
+    in radians a position, pairs (i, i + rot_dim / 2) or, interleaved, (2i,
+    2i + 1), and a factor on cos and sin."""
+
+    __slots__ = ("inv_freq", "rot_dim", "interleaved", "scale")
+
+    def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
+        _dev(inv_freq, "inv_freq", torch.float32)
+        if inv_freq.dim() != 1:
+            raise ValueError("inv_freq must be 1-D")
+        self.inv_freq, self.rot_dim = inv_freq, 2 * inv_freq.numel()
+        self.interleaved, self.scale = bool(interleaved), float(scale)
+
+
+def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, device) -> _CHeads:
+    if x.dtype is not dtype or out.dtype is not dtype or weight is not None and weight.dtype is not dtype:
+        raise TypeError("%s, its weight and its output must share q's dtype" % name)
+    if x.device != device or out.device != device or weight is not None and weight.device != device:
+        raise ValueError("%s, its weight and its output must be on q's device" % name)
+    M, H, D = shape
+    if out.shape != shape:
+        raise ValueError("%s's output must be [%d, %d, %d]" % (name, M, H, D))
+    lr, lh, unit = x.stride()
+    lor, loh, ounit = out.stride()
+    if D > 1 and (unit != 1 or ounit != 1):
+        raise ValueError("%s and its output must have unit stride along their last dimension" % name)
+    wp = None
+    if weight is not None:
+        if weight.shape != (D,) or not weight.is_contiguous():
+            raise ValueError("%s's weight must be a contiguous [%d] tensor" % (name, D))
+        wp = weight.data_ptr()
+    return _CHeads(H, x.data_ptr(), lr, lh, wp, out.data_ptr(), lor, loh)
+
+
+def lora_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
+                      positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                      q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                      eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                      k_out: Optional[torch.Tensor] = None, stream=None):
+    """Norm of each head of q [M, Hq, D] and k [M, Hk, D] (where it has a
+    weight [D]) and rotation by positions (int64 [M]) in one pass; returns the
+    two outputs.  q_out and k_out may be q and k themselves.  Rows with a
+    negative position are left as they are: of outputs made here, unset."""
+    lib = _lib or load_library()
+    dtype, device = q.dtype, q.device
+    dt = _DTYPES.get(dtype)
+    if dt is None:
+        raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
+    if q.dim() != 3 or not q.is_cuda:
+        raise ValueError("q must be a 3-D device tensor")
+    M, _, D = shape = q.shape
+    if q_out is None:
+        q_out = _empty(shape, dtype, device, stream)
+    cq = _head_set(q, "q", q_weight, q_out, shape, dtype, device)
+    ck = None
+    if k is not None:
+        if k.dim() != 3 or k.shape[0] != M or k.shape[2] != D:
+            raise ValueError("k must be [%d, heads, %d]" % (M, D))
+        if k_out is None:
+            k_out = _empty(k.shape, dtype, device, stream)
+        ck = ctypes.byref(_head_set(k, "k", k_weight, k_out, k.shape, dtype, device))
+    cr = None
+    if rope is not None:
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+        if positions.dtype is not torch.int64:
+            raise TypeError("positions must be int64")
+        if positions.shape != (M,) or positions.device != device or not positions.is_contiguous():
+            raise ValueError("positions must be a contiguous [%d] tensor on q's device" % M)
+        _same_device(rope.inv_freq, "inv_freq", device)
+        cr = ctypes.byref(_CRope(positions.data_ptr(), rope.inv_freq.data_ptr(), rope.rot_dim,
+                                 rope.interleaved, rope.scale))
+    _on(device, stream, lib.lora_qk_norm_rope, "lora_qk_norm_rope", dt, M, D, eps, ctypes.byref(cq), ck, cr)
+    return q_out, k_out
 
 
 def lora_merge(W: torch.Tensor, adapters: Adapters, adapter: int, scales: torch.Tensor,

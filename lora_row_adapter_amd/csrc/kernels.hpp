@@ -6,6 +6,8 @@
 
 #include "lora_row.h"
 #include "lora_mx.h"
+#include "lora_w4.h"
+#include "lora_heads.h"
 #include "common.hpp"
 
 namespace lora {
@@ -219,6 +221,60 @@ hipError_t launch_gemm_mx(const MxGemmArgs &a, hipStream_t st);
 // Index of the tile shape it takes (of the first slab); out: its rows, columns
 // and the elements of k that the longest of its LDS rings holds.
 int gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t xfmt, int32_t out[3]);
+// A 4-bit weight with group scales and zero points (lora_w4.h).  Laid out in
+// records of 16 rows by 128 columns, the records of 16 rows one after another:
+//   1024 bytes of codes: dword i of lane l's 16 bytes holds row l % 16, columns
+//     32 i + 8 (l / 16) + 0 .. 7, column 2p in bits 4p .. 4p + 3 and column
+//     2p + 1 in bits 16 + 4p ..: what lane l hands the matrix instruction in
+//     its i-th step of 32 columns, two shifts and masks away from bf16;
+//   16 words for each group in the record (1, 2 or 4; a group past 128 columns
+//     is repeated): the fp32 scale of a row, its low five bits the zero point.
+// Rows past d and groups past k have a scale of zero, columns past k any code.
+struct W4Args {
+  int64_t d, k;
+  int32_t group, nb, sg;  // nb: records a row; sg: groups a record
+  const uint8_t *q;
+  int64_t ldq;
+  int32_t scale_dtype;
+  const void *scales;
+  int64_t lds;
+  const uint8_t *zeros;
+  int64_t ldz;
+  uint8_t *w;
+  int32_t dtype;  // of y
+  void *y;
+  int64_t ldy;
+};
+constexpr int64_t kW4Codes = 1024;
+constexpr int64_t w4_record(int32_t sg) { return kW4Codes + 64 * sg; }
+hipError_t launch_w4_pack(const W4Args &a, hipStream_t st);
+hipError_t launch_w4_dequantize(const W4Args &a, hipStream_t st);
+struct W4GemmArgs {
+  int32_t M, N, K, nb, sg;
+  const uint16_t *x;
+  int64_t ldx;
+  const uint8_t *w;
+  uint16_t *y;
+  int64_t ldy;
+};
+hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st);
+// Norm and rotation of heads (lora_heads.h).
+struct HeadSet {
+  const void *x, *w;
+  void *out;
+  int64_t ldr, ldh, ldor, ldoh;
+  int32_t n;
+};
+struct HeadsArgs {
+  int32_t dtype;
+  int64_t M;
+  int32_t D, rot, interleaved;
+  float eps, scale;
+  HeadSet s[2];
+  const int64_t *pos;      // nullptr: no rotation
+  const float *inv_freq;
+};
+hipError_t launch_heads(const HeadsArgs &a, hipStream_t st);
 hipError_t launch_shrink_gather(const LoraArgs &a, hipStream_t st);
 hipError_t launch_expand_gather(const LoraArgs &a, hipStream_t st);
 // A rows per stage the LDS-staged SGMV shrink takes for this launch (per
@@ -299,6 +355,17 @@ struct MxBase {
   int32_t x_format;
   const lora_norm_t *norm;
 };
+// 4-bit base of the layer.
+struct W4Base {
+  const lora_w4_t *W;
+};
+lora_status_t check_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                            const lora_w4_t *W, const void *y, int64_t ldy, const void *workspace,
+                            size_t workspace_bytes);
+// One launch or more of y = x W^T; ws may be nullptr.
+hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                       const lora_w4_t *W, void *y, int64_t ldy, void *ws, size_t ws_bytes,
+                       hipStream_t st);
 // Optional per-kernel timing (lora_profile_*; defined in lora_api.cpp).
 namespace prof {
 int begin(int c, hipStream_t st);
@@ -332,8 +399,9 @@ struct MxLayout {
 };
 MxLayout mx_layout(int64_t rows, int64_t k, int32_t x_format);
 
-// The multi-slice layer behind lora_linear_sliced(_q, _mx) (the C ABI's types;
-// defined in lora_api.cpp).  mx: a microscaled base in place of W.
+// The multi-slice layer behind lora_linear_sliced(_q, _mx, _w4) (the C ABI's
+// types; defined in lora_api.cpp).  mx, w4: a microscaled or 4-bit base in
+// place of W.
 // self_contained: create no library resource -- the plan runs on the caller's
 // stream and no launch is timed.
 lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const void *x,
@@ -341,6 +409,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                                  int32_t n_slices, const lora_slice_t *slices,
                                  const int32_t *adapter_ids, void *y, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, int32_t path, uint32_t flags, void *stream,
-                                 bool self_contained, const MxBase *mx = nullptr);
+                                 bool self_contained, const MxBase *mx = nullptr,
+                                 const W4Base *w4 = nullptr);
 
 }  // namespace lora

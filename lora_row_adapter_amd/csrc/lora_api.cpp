@@ -535,8 +535,8 @@ static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d
 }
 
 // The layer over several slices; the base weight is dense (W, ldw) or, with
-// qw != nullptr, quantized, or with mx != nullptr microscaled (both bf16
-// only).  self_contained: use no library
+// qw != nullptr, quantized, with mx != nullptr microscaled or with w4 !=
+// nullptr 4-bit (all bf16 only).  self_contained: use no library
 // resource that may need creating -- the plan runs on the caller's stream
 // (no side stream or fork/join events) and no launch is timed.
 lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const void *x,
@@ -544,13 +544,14 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                                  int32_t n_slices, const lora_slice_t *slices,
                                  const int32_t *adapter_ids, void *y, int64_t ldy, void *workspace,
                                  size_t workspace_bytes, int32_t path, uint32_t flags, void *stream,
-                                 bool self_contained, const MxBase *mx) {
+                                 bool self_contained, const MxBase *mx, const W4Base *w4) {
   int32_t S = 0, R = 0;
   int64_t d_total = 0;
   if (slices == nullptr || n_slices < 1 || n_slices > LORA_MAX_SLICES) return LORA_ERR_ARG;
   lora_status_t s = check_slices(n_slices, slices, M, &S, &R, &d_total);
   if (s != LORA_OK) return s;
   s = mx   ? check_mx_layer(*mx, M, k, d_total, x, ldx, y, ldy, workspace, workspace_bytes)
+      : w4 ? check_gemm_w4(M, k, d_total, x, ldx, w4->W, y, ldy, workspace, workspace_bytes)
       : qw ? check_q_gemm_args(M, k, d_total, x, ldx, qw, y, ldy)
            : check_gemm_args(dtype, M, k, d_total, x, ldx, W, ldw, y, ldy);
   if (s != LORA_OK) return s;
@@ -566,7 +567,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
   if (workspace_bytes < ws_layout(first, S, R, n_slices).total +
                             (mx ? mx_layout(first, k, mx->x_format).total : 0))
     return LORA_ERR_WORKSPACE;
-  const bool dense = !qw && !mx;  // the base GEMM that can carry plan and shrink
+  const bool dense = !qw && !mx && !w4;  // the base GEMM that can carry plan and shrink
 
   // kernel family: MFMA tiles need bf16 operands and ranks <= 64
   const bool mfma_ok = dtype == LORA_DTYPE_BF16 && R <= kMaxRankMfma;
@@ -742,6 +743,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
       if (mx)
         return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL,
                            in_prep ? &gplan : nullptr, st);
+      if (w4) return run_gemm_w4(Mc, k, d_total, xc, ldx, w4->W, yc, ldy, gws, gws_bytes, st);
       if (qw) return launch_gemm_q(make_q_args(qw, Mc, k, d_total, xc, ldx, yc, ldy), st);
       // expired split-K waits are counted in the plan header, where
       // lora_check reads them
