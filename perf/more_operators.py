@@ -175,20 +175,18 @@ def _handles(st):
         st["rope"] = lr.Rope(st["inv_freq"], interleaved=case["interleaved"])
         return
     st["W"] = lr.lora_w4_pack(st["Wq"], st["Ws"], case["k"], case["group"], zeros=st["Wz"])
-    if case["kind"] == "product":
-        n = lr.gemm_w4_workspace_bytes(case["M"], case["k"], case["d"])
-    else:
+    if case["kind"] == "layer":
         st["slices"] = [lr.Slice(case["d"], lr.Adapters.slots(st["A"], st["B"], st["ranks"]), st["scales"])]
         if case["d2"]:
             st["slices"].append(lr.Slice(case["d2"], lr.Adapters.slots(st["A2"], st["B2"], st["ranks"]), st["scales"]))
         n = lr.workspace_bytes_sliced_w4(case["M"], case["k"], st["slices"])
-    st["workspace"] = torch.zeros(n, dtype=torch.uint8, device="cuda")
+        st["workspace"] = torch.zeros(n, dtype=torch.uint8, device="cuda")
 
 
 def _run_own(st):
     lr, kind = st["lr"], st["case"]["kind"]
     if kind == "product":
-        return lr.lora_gemm_w4(st["x"], st["W"], workspace=st["workspace"])
+        return lr.lora_gemm_w4(st["x"], st["W"])
     if kind == "layer":
         return lr.lora_linear_sliced_w4(st["x"], st["W"], st["slices"], st["ids"], workspace=st["workspace"])
     q, k = lr.lora_qk_norm_rope(st["q"], st["k"], st["positions"], st["rope"], q_weight=st["wq"], k_weight=st["wk"], eps=EPS)
