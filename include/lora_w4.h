@@ -71,27 +71,24 @@ lora_status_t lora_w4_dequantize(lora_dtype_t dtype, int64_t d, int64_t k, const
                                  void *y, int64_t ldy, void *stream);
 
 /*
- * Bytes of workspace with which lora_gemm_w4 is fastest for this size (0:
- * none; never more than 256 MiB and that of lora_gemm).  Host-only.
- */
-size_t lora_gemm_w4_workspace_bytes(int64_t M, int64_t k, int64_t d);
-
-/*
  * y = x W^T: x bf16 [M, k] (k, ldx multiples of 8, 16-byte aligned), y bf16
- * [M, d] (ldy >= d).  Codes meet x exactly; each group's sum is scaled and
- * added in fp32, y rounded once.  Where a workspace of
- * lora_gemm_w4_workspace_bytes(M, k, d) bytes (256-byte aligned, no
- * initialisation) is given and that is not 0, the weight is read back into it
- * as bf16, each weight rounded once, and multiplied as lora_gemm does; smaller
- * or NULL: the first form.  Sums that leave fp32's range on the way (|x| past
- * 2^120 or so) and infinities in x may become NaN in their row.
- * Deterministic: the summation order depends on the sizes alone (and on
- * whether there is a workspace).  y must not overlap x, W or the workspace
- * (LORA_ERR_ARG).
+ * [M, d] (ldy >= d).  Up to some hundred rows codes meet x exactly, and each
+ * group's sum is scaled and added in fp32; past that the weights are rounded to
+ * bf16, once each, ahead of the product (which of the two is a matter of the
+ * sizes alone: lora_test_gemm_w4_shape).  y is rounded once.  Sums that leave
+ * fp32's range on the way (|x| past 2^120 or so) and infinities in x may become
+ * NaN in their row.  Deterministic: the summation order depends on the sizes
+ * alone.  y must not overlap x or W (LORA_ERR_ARG).
  */
 lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                           const lora_w4_t *W, void *y, int64_t ldy, void *workspace,
-                           size_t workspace_bytes, void *stream);
+                           const lora_w4_t *W, void *y, int64_t ldy, void *stream);
+
+/*
+ * Testing hook: which of the product's tile shapes a size takes (their order
+ * is the library's own; -1: invalid arguments).  Host-only.  out[0], out[1]:
+ * the tile's rows of x and of W; out[2]: 1 where it rounds the weights to bf16.
+ */
+int32_t lora_test_gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t group, int32_t out[3]);
 
 /*
  * Bytes of workspace lora_linear_sliced_w4 needs for up to max_rows rows (any

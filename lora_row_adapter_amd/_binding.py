@@ -237,10 +237,10 @@ def load_library():
     lib.lora_w4_pack.restype = i32
     lib.lora_w4_dequantize.argtypes = [i32, i64, i64, pw4, p, i64, p]
     lib.lora_w4_dequantize.restype = i32
-    lib.lora_gemm_w4_workspace_bytes.argtypes = [i64, i64, i64]
-    lib.lora_gemm_w4_workspace_bytes.restype = sz
-    lib.lora_gemm_w4.argtypes = [i64, i64, i64, p, i64, pw4, p, i64, p, sz, p]
+    lib.lora_gemm_w4.argtypes = [i64, i64, i64, p, i64, pw4, p, i64, p]
     lib.lora_gemm_w4.restype = i32
+    lib.lora_test_gemm_w4_shape.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i32)]
+    lib.lora_test_gemm_w4_shape.restype = i32
     lib.lora_workspace_bytes_sliced_w4.argtypes = [i64, i64, i32, psl]
     lib.lora_workspace_bytes_sliced_w4.restype = sz
     lib.lora_linear_sliced_w4.argtypes = [i64, i64, p, i64, pw4, i32, psl, p, p, i64, p, sz, i32, u32, p]
@@ -1204,15 +1204,9 @@ def lora_w4_dequantize(W: W4, dtype: torch.dtype = torch.bfloat16, out: Optional
     return out
 
 
-def gemm_w4_workspace_bytes(M: int, k: int, d: int) -> int:
-    """Workspace bytes with which lora_gemm_w4 is fastest (0: none)."""
-    return int(load_library().lora_gemm_w4_workspace_bytes(int(M), int(k), int(d)))
-
-
 def lora_gemm_w4(x: torch.Tensor, W: W4, y: Optional[torch.Tensor] = None,
-                 workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """y = x W^T (bfloat16 x [M, k] and y [M, d]).  Without a workspace one of
-    gemm_w4_workspace_bytes bytes is allocated (torch) for the call."""
+                 stream=None) -> torch.Tensor:
+    """y = x W^T (bfloat16 x [M, k] and y [M, d])."""
     lib = _lib or load_library()
     bf = torch.bfloat16
     if x.dtype is not bf:
@@ -1226,15 +1220,18 @@ def lora_gemm_w4(x: torch.Tensor, W: W4, y: Optional[torch.Tensor] = None,
         yp, ldy = y.data_ptr(), W.d
     else:
         yp, ldy = _matrix(y, "y", (M, W.d), bf, device)
-    if workspace is None:
-        n = lib.lora_gemm_w4_workspace_bytes(M, k, W.d)
-        if n > 0:
-            workspace = _empty(n, torch.uint8, device, stream)
-    else:
-        _same_device(workspace, "workspace", device)
-    wp, wn = (None, 0) if workspace is None else (_dev(workspace, "workspace", torch.uint8), workspace.numel())
-    _on(device, stream, lib.lora_gemm_w4, "lora_gemm_w4", M, k, W.d, xp, ldx, W._ref, yp, ldy, wp, wn)
+    _on(device, stream, lib.lora_gemm_w4, "lora_gemm_w4", M, k, W.d, xp, ldx, W._ref, yp, ldy)
     return y
+
+
+def test_gemm_w4_shape(M: int, k: int, d: int, group: int):
+    """Testing hook: (index, rows, columns, 1 if it rounds the weights) of the
+    tile shape that lora_gemm_w4 takes."""
+    out = (ctypes.c_int32 * 3)()
+    i = load_library().lora_test_gemm_w4_shape(int(M), int(k), int(d), int(group), out)
+    if i < 0:
+        raise LoraError(1, "lora_test_gemm_w4_shape")
+    return (i,) + tuple(out)
 
 
 def workspace_bytes_sliced_w4(max_rows: int, k: int, slices) -> int:

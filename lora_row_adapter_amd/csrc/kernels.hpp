@@ -224,9 +224,9 @@ int gemm_mx_shape(int64_t M, int64_t k, int64_t d, int32_t xfmt, int32_t out[3])
 // A 4-bit weight with group scales and zero points (lora_w4.h).  Laid out in
 // records of 16 rows by 128 columns, the records of 16 rows one after another:
 //   1024 bytes of codes: dword i of lane l's 16 bytes holds row l % 16, columns
-//     32 i + 8 (l / 16) + 0 .. 7, column 2p in bits 4p .. 4p + 3 and column
-//     2p + 1 in bits 16 + 4p ..: what lane l hands the matrix instruction in
-//     its i-th step of 32 columns, two shifts and masks away from bf16;
+//     32 i + 8 (l / 16) + 0 .. 7 (column c in the low nibble of byte c for c <
+//     4, in the high one of byte c - 4 else): what lane l hands the matrix
+//     instruction in its i-th step of 32 columns, a mask from E4M3 bytes;
 //   16 words for each group in the record (1, 2 or 4; a group past 128 columns
 //     is repeated): the fp32 scale of a row, its low five bits the zero point.
 // Rows past d and groups past k have a scale of zero, columns past k any code.
@@ -256,8 +256,12 @@ struct W4GemmArgs {
   const uint8_t *w;
   uint16_t *y;
   int64_t ldy;
+  int32_t tiles_m, tiles_n;
 };
 hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st);
+// Index of the tile shape it takes; out: its rows, columns and whether it rounds
+// the weights to bf16.
+int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]);
 // Norm and rotation of heads (lora_heads.h).
 struct HeadSet {
   const void *x, *w;
@@ -359,13 +363,12 @@ struct MxBase {
 struct W4Base {
   const lora_w4_t *W;
 };
+// workspace: the layer's, or nullptr
 lora_status_t check_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
                             const lora_w4_t *W, const void *y, int64_t ldy, const void *workspace,
                             size_t workspace_bytes);
-// One launch or more of y = x W^T; ws may be nullptr.
 hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                       const lora_w4_t *W, void *y, int64_t ldy, void *ws, size_t ws_bytes,
-                       hipStream_t st);
+                       const lora_w4_t *W, void *y, int64_t ldy, hipStream_t st);
 // Optional per-kernel timing (lora_profile_*; defined in lora_api.cpp).
 namespace prof {
 int begin(int c, hipStream_t st);

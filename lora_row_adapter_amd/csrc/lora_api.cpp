@@ -743,7 +743,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
       if (mx)
         return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL,
                            in_prep ? &gplan : nullptr, st);
-      if (w4) return run_gemm_w4(Mc, k, d_total, xc, ldx, w4->W, yc, ldy, gws, gws_bytes, st);
+      if (w4) return run_gemm_w4(Mc, k, d_total, xc, ldx, w4->W, yc, ldy, st);
       if (qw) return launch_gemm_q(make_q_args(qw, Mc, k, d_total, xc, ldx, yc, ldy), st);
       // expired split-K waits are counted in the plan header, where
       // lora_check reads them

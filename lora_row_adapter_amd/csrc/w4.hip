@@ -2,13 +2,13 @@
 // it back, and the product
 //   y[m, n] = sum_g s[n, g] (sum_{j in g} x[m, j] q[n, j] - z[n, g] sum_{j in g} x[m, j])
 //
-// A code needs one mask and one OR to be a bf16 number: 0x4300 | q is 128 + q
-// exactly, so the matrix instruction multiplies x with 128 + q and, against a
-// column of ones, gives the group's sum of x; then
-//   tot += s (acc - (128 + z) X)
-// in fp32: no weight is rounded.  acc and (128 + z) X are about 143 / 4.6
-// times what is left of them (codes are 4.6 off their zero point, root mean
-// square), which costs the sum 5 of fp32's 24 bits; y keeps 8.
+// A code in a byte is an E4M3 number, q 2^-9 exactly (subnormals and the first
+// binade lie on one line), so gfx950's scaled conversion turns two codes into
+// two bf16 in one instruction at the full rate: seven instructions for eight
+// codes.  The matrix instruction multiplies them with x as they are, and x
+// with a column of ones for the group's sum X of x; then
+//   tot += s (acc - z X)
+// in fp32: no weight is rounded.
 #include <algorithm>
 
 #include "kernels.hpp"
@@ -19,12 +19,15 @@ namespace {
 
 __device__ __forceinline__ float scale_of(uint32_t w) { return __uint_as_float(w & ~31u); }
 
-// 128 + codes of one dword as the matrix instruction's eight bf16.
-__device__ __forceinline__ bf16x8_t codes128(uint32_t w) {
-  u32x4_t v;
-#pragma unroll
-  for (int p = 0; p < 4; ++p) v[p] = ((w >> (4 * p)) & 0x000F000Fu) | 0x43004300u;
-  return __builtin_bit_cast(bf16x8_t, v);
+// The codes of one dword as the matrix instruction's eight bf16: columns 0 - 3
+// from the low nibbles of its bytes, 4 - 7 from the high ones.
+__device__ __forceinline__ bf16x8_t codes(uint32_t w) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 512.f, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 512.f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
 // ---------------------------------------------------------------- layout
@@ -39,11 +42,12 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4Args a) {
   if (n < a.d) {
     const uint8_t *row = a.q + n * a.ldq;
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
+    for (int p = 0; p < 4; ++p) {  // columns 2p and 2p + 1
       const int64_t j = j0 + 2 * p;
       if (j < a.k) {
         const uint32_t b = row[j >> 1];
-        w |= (b & 15u) << (4 * p) | (b >> 4) << (16 + 4 * p);
+        const int at = 16 * (p & 1) + 4 * (p >> 1);
+        w |= (b & 15u) << at | (b >> 4) << (at + 8);
       }
     }
   }
@@ -66,54 +70,247 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4Args a) {
   }
 }
 
-// One workgroup a record, a dword of codes (eight columns of a row) a thread;
-// sixteen threads cover a row's 128 columns.
+// A workgroup reads kDqRecords records of 16 rows back; of each, a thread takes
+// a dword of codes (eight columns of a row) and sixteen threads a row's 128
+// columns.  All of a thread's loads go ahead of its stores.
+constexpr int kDqRecords = 8;
 template <typename T>
-__global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a) {
-  const int64_t rec = blockIdx.x, tile = rec / a.nb, blk = rec - tile * a.nb;
-  const uint32_t *in = reinterpret_cast<const uint32_t *>(a.w + rec * w4_record(a.sg));
+__global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, int32_t per_row) {
+  const int64_t tile = blockIdx.x / per_row;
+  const int blk0 = (int)(blockIdx.x - tile * per_row) * kDqRecords;
+  const uint8_t *in = a.w + (tile * a.nb + blk0) * w4_record(a.sg);
   const int t = threadIdx.x, row = t >> 4, i = (t >> 2) & 3, h = t & 3;
-  const int64_t n = tile * 16 + row, j0 = blk * 128 + 32 * i + 8 * h;
-  if (n >= a.d || j0 >= a.k) return;
-  const uint32_t w = in[(h * 16 + row) * 4 + i];
-  const uint32_t sw = in[256 + (i * a.sg >> 2) * 16 + row];
-  const float s = scale_of(sw);
-  const int z = (int)(sw & 31u);
-  // 19 bits by 5: the products are exact
-  float v[8];
+  const int64_t n = tile * 16 + row;
+  if (n >= a.d) return;
+  const int at = ((h * 16 + row) * 4 + i) * 4, sat = (int)kW4Codes + ((i * a.sg >> 2) * 16 + row) * 4;
+  uint32_t w[kDqRecords], sw[kDqRecords];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    v[2 * p] = s * (float)((int)((w >> (4 * p)) & 15u) - z);
-    v[2 * p + 1] = s * (float)((int)((w >> (16 + 4 * p)) & 15u) - z);
+  for (int r = 0; r < kDqRecords; ++r) {
+    const uint8_t *rec = in + min(r, a.nb - 1 - blk0) * w4_record(a.sg);
+    w[r] = *reinterpret_cast<const uint32_t *>(rec + at);
+    sw[r] = *reinterpret_cast<const uint32_t *>(rec + sat);
   }
-  T *y = (T *)a.y + n * a.ldy + j0;
-  const int left = (int)min((int64_t)8, a.k - j0);
-  T o[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    if constexpr (sizeof(T) == 2) o[e] = f32_to_bf16_bits(v[e]);
-    else o[e] = v[e];
-  }
-  if (left == 8 && ((uintptr_t)y & 15) == 0) {
+  for (int r = 0; r < kDqRecords; ++r) {
+    const int64_t j0 = (int64_t)(blk0 + r) * 128 + 32 * i + 8 * h;
+    if (j0 >= a.k) return;
+    const float s = scale_of(sw[r]);
+    const int z = (int)(sw[r] & 31u);
+    // 19 bits by 5: the products are exact
+    T o[8];
 #pragma unroll
-    for (int c = 0; c < (int)sizeof(T) / 2; ++c)
-      reinterpret_cast<uint4 *>(y)[c] = reinterpret_cast<const uint4 *>(o)[c];
-  } else {
-    for (int e = 0; e < left; ++e) y[e] = o[e];
+    for (int e = 0; e < 8; ++e) {
+      const float v = s * (float)((int)((w[r] >> (8 * (e & 3) + (e & 4))) & 15u) - z);
+      if constexpr (sizeof(T) == 2) o[e] = f32_to_bf16_bits(v);
+      else o[e] = v;
+    }
+    T *y = (T *)a.y + n * a.ldy + j0;
+    const int left = (int)min((int64_t)8, a.k - j0);
+    if (left == 8 && ((uintptr_t)y & 15) == 0) {
+#pragma unroll
+      for (int c = 0; c < (int)sizeof(T) / 2; ++c)
+        reinterpret_cast<uint4 *>(y)[c] = reinterpret_cast<const uint4 *>(o)[c];
+    } else {
+      for (int e = 0; e < left; ++e) y[e] = o[e];
+    }
   }
 }
 
-// ---------------------------------------------------------------- product
-// A workgroup takes 16 rows of x and 16 of W, its four waves every fourth
-// record of k.
+// ---------------------------------------------------------------- few rows
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+constexpr uint32_t kOob = 0xFFFFFFF0u;  // past every buffer: loads give zeros
+
+__device__ __forceinline__ bf16x8_t ones8() {
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, bytes, 0x00020000);
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+__device__ __forceinline__ uint32_t lds_addr(const void *p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)p;
+}
+// The fragments of FM 16-row tiles for two steps of 32 columns, at a0 and a1
+// and 2 KiB on for each tile, and the wait for them: one statement, as the
+// compiler would wait for every load into LDS ahead of a read of its own.
+template <int FM>
+__device__ __forceinline__ void read_half(uint32_t a0, uint32_t a1, u32x4_t (&x)[2][FM]) {
+  static_assert(FM == 1 || FM == 2 || FM == 4, "tiles");
+  if constexpr (FM == 1)
+    asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(x[0][0]), "=&v"(x[1][0]) : "v"(a0), "v"(a1) : "memory");
+  else if constexpr (FM == 2)
+    asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:2048\n\t"
+                 "ds_read_b128 %2, %5\n\tds_read_b128 %3, %5 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[1][0]), "=&v"(x[1][1]) : "v"(a0), "v"(a1) : "memory");
+  else
+    asm volatile("ds_read_b128 %0, %8\n\tds_read_b128 %1, %8 offset:2048\n\tds_read_b128 %2, %8 offset:4096\n\t"
+                 "ds_read_b128 %3, %8 offset:6144\n\tds_read_b128 %4, %9\n\tds_read_b128 %5, %9 offset:2048\n\t"
+                 "ds_read_b128 %6, %9 offset:4096\n\tds_read_b128 %7, %9 offset:6144\n\ts_waitcnt lgkmcnt(0)"
+                 : "=&v"(x[0][0]), "=&v"(x[0][1]), "=&v"(x[0][2]), "=&v"(x[0][3]), "=&v"(x[1][0]), "=&v"(x[1][1]),
+                   "=&v"(x[1][2]), "=&v"(x[1][3]) : "v"(a0), "v"(a1) : "memory");
+}
+
+// A workgroup takes 16 FM rows of x and 16 FN of W, each of its NW waves every
+// NW-th record of k.  No wave shares an operand with another, so nothing waits
+// but for its own loads, and the waves of a SIMD drift apart: one unpacks while
+// the other multiplies.  W's records go straight to registers, x's rows by
+// direct loads through the wave's own part of LDS (fragments read from memory
+// would touch sixteen half lines an instruction: 54 cycles of a CU against 35),
+// both PD records ahead.  The waves' sums meet in LDS at the end, in their order.
+// Loads past the end of a wave's records, of x's rows and of its columns are
+// past their buffer: they move nothing and give zeros.
+template <int FM, int FN, int NW, int PD, int SG>
+__global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p) {
+  constexpr int REC = (int)w4_record(SG), KS = 4 / SG;
+  constexpr int HALF = FM * 2048, XI = 2 * FM;  // x: bytes of half a record, loads of 1 KiB
+  constexpr int RING = NW * PD * 2 * HALF, PART = NW * FM * FN * 1024;
+  constexpr int kYounger = XI + (PD - 1) * (FN * (1 + SG) + 2 * XI) + FN * (1 + SG);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max(RING, PART)];
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * (16 * FN), m0 = blockIdx.y * (16 * FM);
+  const int mr = min(16 * FM, p.M - m0), nr = min(16 * FN, p.N - n0);
+  const uint32_t tile_bytes = (uint32_t)p.nb * REC;
+  const auto rx = rsrc(p.x + (int64_t)m0 * p.ldx, (uint32_t)(((mr - 1) * p.ldx + p.K) * 2));
+  const auto rw = rsrc(p.w + (int64_t)(n0 / 16) * tile_bytes, (uint32_t)((nr + 15) / 16) * tile_bytes);
+  const int cnt = wave < p.nb ? (p.nb - 1 - wave) / NW + 1 : 0;  // this wave's records
+
+  // x: eight rows a load, 128 bytes each; chunk c of row i stands at c ^ (i & 7)
+  const int cx = ((lane & 7) ^ (lane >> 3)) * 8;
+  const uint32_t vx = (uint32_t)((lane >> 3) * p.ldx * 2 + cx * 2), row8 = (uint32_t)(8 * p.ldx * 2);
+  uint8_t *ring = smem + wave * (PD * 2 * HALF);
+  auto load_x = [&](int t, int d, int u) {
+    const int k0 = (wave + t * NW) * 128 + 64 * u;
+    const uint32_t v = t < cnt && k0 + cx < p.K ? vx : kOob;
+#pragma unroll
+    for (int q = 0; q < XI; ++q)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rx, (__attribute__((address_space(3))) void *)(ring + (d * 2 + u) * HALF + q * 1024), 16, v,
+          (uint32_t)k0 * 2 + q * row8, 0, 0);
+  };
+  u32x4_t wq[PD][FN];
+  uint32_t sq[PD][FN][SG];
+  auto load_w = [&](int t, int d) {
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      const uint32_t at = t < cnt ? j * tile_bytes + (uint32_t)(wave + t * NW) * REC : kOob;
+      wq[d][j] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rw, lane * 16, at, 0));
+#pragma unroll
+      for (int g = 0; g < SG; ++g)
+        sq[d][j][g] = __builtin_amdgcn_raw_buffer_load_b32(rw, r * 4 + (int)kW4Codes + 64 * g, at, 0);
+    }
+  };
+  f32x4_t tot[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) tot[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
+  const uint32_t xa = lds_addr(ring) + r * 128;
+#pragma unroll
+  for (int d = 0; d < PD; ++d) {
+    load_w(d, d);
+    asm volatile("" ::: "memory");
+    load_x(d, d, 0);
+    load_x(d, d, 1);
+    asm volatile("" ::: "memory");
+  }
+  for (int t0 = 0; t0 < cnt; t0 += PD) {
+#pragma unroll
+    for (int d = 0; d < PD; ++d) {  // past the last record: zeros by zeros
+      u32x4_t wc[FN];
+      float s[FN][SG], z[FN][SG];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        wc[j] = wq[d][j];
+#pragma unroll
+        for (int g = 0; g < SG; ++g) {
+          s[j][g] = scale_of(sq[d][j][g]);
+          z[j][g] = (float)(sq[d][j][g] & 31u);
+        }
+      }
+      load_w(t0 + d + PD, d);
+      f32x4_t acc[FM][FN], sum[FM];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        // Loads younger than this half's: the other half's of the same record or
+        // the one before, W's and x's of the records between, W's just above.
+        asm volatile("" ::: "memory");
+        wait_vm<std::min(kYounger, 63)>();
+        u32x4_t xf[2][FM];
+        const uint32_t at = xa + (d * 2 + u) * HALF;
+        read_half<FM>(at + (h ^ (r & 7)) * 16, at + ((4 + h) ^ (r & 7)) * 16, xf);
+        load_x(t0 + d + PD, d, u);
+        asm volatile("" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int ks = 2 * u + i, g = ks / KS;
+          const bool first = ks % KS == 0, last = ks % KS == KS - 1;
+#pragma unroll
+          for (int m = 0; m < FM; ++m)
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), ones8(),
+                                                             first ? zero : sum[m], 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            const bf16x8_t wf = codes(wc[j][ks]);
+#pragma unroll
+            for (int m = 0; m < FM; ++m) {
+              acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), wf,
+                                                                  first ? zero : acc[m][j], 0, 0, 0);
+              if (last) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  tot[m][j][e] = __builtin_fmaf(s[j][g], __builtin_fmaf(-z[j][g], sum[m][e], acc[m][j][e]), tot[m][j][e]);
+              }
+            }
+          }
+        }
+      }
+    }
+  }
+  wait_vm<0>();  // loads past the end have landed: LDS is free
+  __syncthreads();
+  f32x4_t(*part)[FM * FN][64] = reinterpret_cast<f32x4_t(*)[FM * FN][64]>(smem);
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) part[wave][m * FN + j][lane] = tot[m][j];
+  __syncthreads();
+  for (int u = wave; u < FM * FN; u += NW) {
+    f32x4_t v = part[0][u][lane];
+#pragma unroll
+    for (int q = 1; q < NW; ++q) v += part[q][u][lane];
+    const int n = n0 + u % FN * 16 + r, m = m0 + u / FN * 16 + 4 * h;
+    if (n >= p.N) continue;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (m + e < p.M) p.y[(int64_t)(m + e) * p.ldy + n] = f32_to_bf16_bits(v[e]);
+  }
+}
+
+template <int FM, int FN, int NW, int PD>
+void launch_split(W4GemmArgs a, hipStream_t st) {
+  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
+  if (a.sg == 1) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 1>), grid, block, 0, st, a);
+  else if (a.sg == 2) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 4>), grid, block, 0, st, a);
+}
+
+// Rows of x past 32-bit offsets of one another (the last tokens of long
+// sequences, say): the same work with x by address, four waves a 16 x 16 tile.
 template <int SG>
-__global__ __launch_bounds__(256) void k_w4_rows(W4GemmArgs p) {
+__global__ __launch_bounds__(256) void k_w4_far(W4GemmArgs p) {
   __shared__ f32x4_t part[3][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, h = lane >> 4;
   const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
   const uint16_t *x = p.x + (int64_t)min(m0 + (lane & 15), p.M - 1) * p.ldx;
   const uint8_t *w = p.w + (int64_t)blockIdx.x * p.nb * w4_record(SG);
-  const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
   f32x4_t tot = {0.f, 0.f, 0.f, 0.f};
   for (int blk = wave; blk < p.nb; blk += 4) {
     const uint8_t *rec = w + (int64_t)blk * w4_record(SG);
@@ -128,11 +325,11 @@ __global__ __launch_bounds__(256) void k_w4_rows(W4GemmArgs p) {
         u32x4_t xv = {0, 0, 0, 0};
         if (j < p.K) xv = *reinterpret_cast<const u32x4_t *>(x + j);
         const bf16x8_t xf = __builtin_bit_cast(bf16x8_t, xv);
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, codes128(c[i]), acc, 0, 0, 0);
-        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones, sum, 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, codes(c[i]), acc, 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, ones8(), sum, 0, 0, 0);
       }
       const uint32_t sw = sc[g * 16];
-      const float s = scale_of(sw), z = (float)(128 + (int)(sw & 31u));
+      const float s = scale_of(sw), z = (float)(sw & 31u);
 #pragma unroll
       for (int e = 0; e < 4; ++e) tot[e] += s * (acc[e] - z * sum[e]);
     }
@@ -149,6 +346,357 @@ __global__ __launch_bounds__(256) void k_w4_rows(W4GemmArgs p) {
   }
 }
 
+// ---------------------------------------------------------------- tiles
+// More rows: WM x WN waves, each FM x FN products of 16 x 16, over BM rows of x
+// and BN of W; KG times as many waves where a workgroup's records of k are
+// shared out over KG groups, whose sums meet in LDS.  x goes through an LDS
+// ring of ST stages (KG tiles of BM rows by 128 columns) by direct loads, W's
+// records straight to the registers of the waves that unpack them, one
+// stage ahead.
+// W is rounded to bf16, s (q - z), before the product: scaling the groups' sums
+// takes eight instructions for every 16 x 16 x group and as many sums again in
+// registers, which tiles of this size have no room for.
+
+// 16 bytes a lane from global memory straight into LDS, lane i's at lds + 16 i
+// (as in gemm_mx.hip: asm, because the compiler would drain every load ahead
+// of each LDS read; the waits are explicit; no register output).
+__device__ __forceinline__ void dma(i32x4_t r, uint32_t lds, uint32_t off, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               : : "s"(lds), "v"(off), "s"(r), "s"(soff));
+}
+__device__ __forceinline__ i32x4_t rsrc_words(const void *p, uint32_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+                 __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+// Waits for this wave's LDS accesses but not for its loads.
+__device__ __forceinline__ void barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Eight weights s (q - z), rounded to bf16 once each: s of 19 bits times z or
+// q - z of five is exact.
+__device__ __forceinline__ bf16x8_t weights(uint32_t w, float s, float sz) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  f32x2_t v[4];
+  v[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, false);
+  v[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.f, true);
+  v[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, false);
+  v[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.f, true);
+  u32x4_t o;
+#pragma unroll
+  for (int p = 0; p < 4; ++p) o[p] = pack_bf16x2(__builtin_fmaf(s, v[p][0], -sz), __builtin_fmaf(s, v[p][1], -sz));
+  return __builtin_bit_cast(bf16x8_t, o);
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG>
+struct WTile {
+  static constexpr int NW = WM * WN * KG, NT = 64 * NW;
+  static constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  static constexpr int XSTAGE = KG * BM * 128;
+  static constexpr int TILES = KG * BN / 16, SB = (TILES + 15) / 16;  // records a stage of W, KiB of its scales a group
+  static constexpr int WSTAGE = TILES * 1024 + SG * SB * 1024;
+  // 1 KiB loads a stage, and a wave's (where there are fewer than waves,
+  // several load the same)
+  static constexpr int XI = XSTAGE / 1024, XL = (XI + NW - 1) / NW;
+  static constexpr int WI = WSTAGE / 1024, WL = (WI + NW - 1) / NW;
+  static constexpr int W0 = ST * XSTAGE;
+  static constexpr int CLD = BN + 8;
+  static constexpr int PART = (KG - 1) * BM * BN * 4;
+  static constexpr int SMEM = std::max(W0 + WS * WSTAGE, std::max(PART, BM * CLD * 2));
+  static_assert(SMEM <= 160 * 1024, "LDS");
+  static_assert(XSTAGE % 1024 == 0 && ST >= 3 && WS >= 2, "stages");
+  static_assert((ST - 1) * XL + ST / 2 * WL < 64, "vmcnt");
+};
+
+// The tile of this workgroup: each XCD takes a contiguous run of tiles, bands
+// of eight row tiles down, then across.
+__device__ __forceinline__ void tile_of(const W4GemmArgs &p, int &tm, int &tn) {
+  const uint32_t nblk = (uint32_t)p.tiles_m * p.tiles_n, b = blockIdx.x;
+  const uint32_t xcd = b & 7, each = nblk >> 3, more = nblk & 7;
+  const uint32_t t = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
+  const uint32_t band = t / (8u * p.tiles_n), in = t - band * 8u * p.tiles_n;
+  const uint32_t rows_in = min(8u, (uint32_t)p.tiles_m - band * 8u);
+  tm = (int)(band * 8u + in % rows_in);
+  tn = (int)(in / rows_in);
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k_w4_tile(W4GemmArgs p) {
+  using T = WTile<FM, FN, WM, WN, KG, ST, WS, SG>;
+  constexpr int BM = T::BM, BN = T::BN, REC = (int)w4_record(SG);
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
+  int tm, tn;
+  tile_of(p, tm, tn);
+  const int m0 = tm * BM, n0 = tn * BN;
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int kg = KG == 1 ? 0 : wave / (WM * WN), wt = KG == 1 ? wave : wave % (WM * WN);
+  const int wm0 = wt / WN * (16 * FM), wn0 = wt % WN * (16 * FN);
+  const int mr = min(BM, p.M - m0), nr = min(BN, p.N - n0);
+  const int nk = (p.nb + KG - 1) / KG;
+  const uint32_t tile_bytes = (uint32_t)p.nb * REC;  // of 16 rows of W
+  i32x4_t rx = rsrc_words(p.x + (int64_t)m0 * p.ldx, (uint32_t)(((mr - 1) * p.ldx + p.K) * 2));
+  i32x4_t rw = rsrc_words(p.w + (int64_t)(n0 / 16) * tile_bytes, (uint32_t)((nr + 15) / 16) * tile_bytes);
+  asm volatile("s_nop 4" : "+s"(rx), "+s"(rw));
+  const uint32_t base = __builtin_amdgcn_readfirstlane(lds_addr(smem));
+
+  // x: eight rows a load, 128 bytes each; chunk c of row i stands at c ^ (i & 7)
+  uint32_t vx[T::XL];
+  int cx[T::XL];
+#pragma unroll
+  for (int i = 0; i < T::XL; ++i) {
+    const int ins = (wave * T::XL + i) % T::XI, row = ins % (BM / 8) * 8 + (lane >> 3);
+    cx[i] = ((lane & 7) ^ (lane >> 3)) * 8 + ins / (BM / 8) * 128;
+    vx[i] = (uint32_t)((row * p.ldx + cx[i]) * 2);
+  }
+  auto load_x = [&](int i, int u) {  // of half record u
+    const int k0 = (u >> 1) * (KG * 128) + (u & 1) * 64;
+    dma(rx, base + u % ST * T::XSTAGE + (wave * T::XL + i) % T::XI * 1024, k0 + cx[i] < p.K ? vx[i] : kOob,
+        (uint32_t)k0 * 2);
+  };
+  // W: the records' codes, a load each, then their scales, sixteen records a
+  // load; those of records past the last one are zero
+  auto load_w = [&](int i, int kt) {
+    const int ins = (wave * T::WL + i) % T::WI;
+    const uint32_t to = base + T::W0 + kt % WS * T::WSTAGE + ins * 1024;
+    if (ins < T::TILES) {
+      const int q = KG == 1 ? 0 : ins / (BN / 16), blk = kt * KG + q;
+      dma(rw, to, blk < p.nb ? lane * 16 : kOob, (uint32_t)(ins - q * (BN / 16)) * tile_bytes + (uint32_t)blk * REC);
+    } else {
+      const int g = (ins - T::TILES) / T::SB, t = (ins - T::TILES) % T::SB * 16 + (lane >> 2);
+      const int q = KG == 1 ? 0 : t / (BN / 16), blk = kt * KG + q;
+      const uint32_t v = (uint32_t)(t - q * (BN / 16)) * tile_bytes + (uint32_t)blk * REC + (lane & 3) * 16;
+      dma(rw, to, t < T::TILES && blk < p.nb ? v : kOob, (uint32_t)(kW4Codes + 64 * g));
+    }
+  };
+  f32x4_t tot[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) tot[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const uint8_t *xb = smem + (kg * BM + wm0 + r) * 128;
+  const uint8_t *wb = smem + T::W0 + (kg * (BN / 16) + wn0 / 16) * 1024 + lane * 16;
+  // Half record s = 2 kt + u is multiplied while the rows of x of half record s +
+  // ST - 1 and, with the even ones, the record kt + WS - 1 of W are loaded, in
+  // that order; the prologue issues what the halves before the first would have.
+#pragma unroll
+  for (int kt = 0; kt < WS - 1; ++kt) {
+    if (2 * (WS - 1 - kt) < ST) continue;
+#pragma unroll
+    for (int i = 0; i < T::WL; ++i) load_w(i, kt);
+  }
+#pragma unroll
+  for (int s = 1 - ST; s < 0; ++s) {
+#pragma unroll
+    for (int i = 0; i < T::XL; ++i) load_x(i, s + ST - 1);
+    if (s % 2 == 0) {
+#pragma unroll
+      for (int i = 0; i < T::WL; ++i) load_w(i, s / 2 + WS - 1);
+    }
+  }
+  // Loads that may be on their way when half record s starts: those of the ST - 2
+  // halves before it -- of the even ones, which turn to another record of W, of
+  // no more than came after that.
+  constexpr int n0h = std::min(ST - 2, 2 * WS - 3), n1h = ST - 2;
+  constexpr int kWait0 = n0h * T::XL + n0h / 2 * T::WL, kWait1 = n1h * T::XL + (n1h + 1) / 2 * T::WL;
+  uint32_t stage = 0;
+  for (int kt = 0; kt < nk; ++kt) {
+    u32x4_t wc[FN];
+    float sc[FN][SG], zc[FN][SG];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u == 0) wait_vm<kWait0>();
+      else wait_vm<kWait1>();
+      barrier();  // every wave's have, and the stage before is free
+      if (u == 0) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          wc[j] = *reinterpret_cast<const u32x4_t *>(wb + kt % WS * T::WSTAGE + j * 1024);
+#pragma unroll
+          for (int g = 0; g < SG; ++g) {
+            const int t = kg * (BN / 16) + wn0 / 16 + j;
+            const uint32_t sw = *reinterpret_cast<const uint32_t *>(
+                smem + T::W0 + kt % WS * T::WSTAGE + (T::TILES + g * T::SB) * 1024 + t * 64 + r * 4);
+            sc[j][g] = scale_of(sw);
+            zc[j][g] = sc[j][g] * (float)(sw & 31u);
+          }
+        }
+      }
+      const int un = 2 * kt + u + ST - 1;  // the half record to load
+      constexpr int nl = T::XL + T::WL;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int ks = 2 * u + i, g = ks * SG / 4;
+        bf16x8_t wf[FN], xf[FM];
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+          xf[m] = *reinterpret_cast<const bf16x8_t *>(xb + stage * T::XSTAGE + m * 2048 + ((i * 4 + h) ^ (r & 7)) * 16);
+        // half of the loads with each step
+#pragma unroll
+        for (int d = i * nl / 2; d < (i + 1) * nl / 2; ++d) {
+          if (d < T::XL) load_x(d, un);
+          else if (u == 0) load_w(d - T::XL, kt + WS - 1);
+        }
+#pragma unroll
+        for (int j = 0; j < FN; ++j) wf[j] = weights(wc[j][ks], sc[j][g], zc[j][g]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int m = 0; m < FM; ++m)
+            tot[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[j], xf[m], tot[m][j], 0, 0, 0);
+      }
+      stage = stage + 1 == ST ? 0 : stage + 1;
+    }
+  }
+  wait_vm<0>();  // the loads past the end have landed: LDS is free
+
+  if constexpr (KG > 1) {  // the groups' sums, in the groups' order
+    __syncthreads();
+    f32x4_t *part = reinterpret_cast<f32x4_t *>(smem);
+    auto at = [&](int q, int i, int j) { return (((q - 1) * WM * WN + wt) * FM * FN + i * FN + j) * 64 + lane; };
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j) part[at(kg, i, j)] = tot[i][j];
+    }
+    __syncthreads();
+    if (kg == 0) {
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int q = 1; q < KG; ++q) tot[i][j] += part[at(q, i, j)];
+    }
+  }
+  __syncthreads();
+  // rounded once and stored, through LDS, as whole rows of 16-byte vectors
+  uint16_t *ct = reinterpret_cast<uint16_t *>(smem);
+  if (kg == 0) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        // lane: row r of x, columns 4 h + e
+        *reinterpret_cast<uint2 *>(ct + (wm0 + i * 16 + r) * T::CLD + wn0 + j * 16 + 4 * h) =
+            make_uint2(pack_bf16x2(tot[i][j][0], tot[i][j][1]), pack_bf16x2(tot[i][j][2], tot[i][j][3]));
+      }
+  }
+  __syncthreads();
+  constexpr int CPR = BN / 8;
+  for (int c = threadIdx.x; c < BM * CPR; c += T::NT) {
+    const int row = c / CPR, col = (c - row * CPR) * 8;
+    if (row >= mr || col >= nr) continue;
+    const uint16_t *src = ct + row * T::CLD + col;
+    uint16_t *dst = p.y + (int64_t)(m0 + row) * p.ldy + n0 + col;
+    if (col + 8 <= nr) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(src);
+      __builtin_memcpy(dst, &v, 16);  // any alignment
+    } else {
+      for (int e = 0; e < 8 && col + e < nr; ++e) dst[e] = src[e];
+    }
+  }
+}
+
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS>
+void launch_tile(W4GemmArgs a, hipStream_t st) {
+  constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
+  a.tiles_m = (a.M + BM - 1) / BM;
+  a.tiles_n = (a.N + BN - 1) / BN;
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(64 * WM * WN * KG);
+  if (a.sg == 1) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 1>), grid, block, 0, st, a);
+  else if (a.sg == 2) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 4>), grid, block, 0, st, a);
+}
+
+// ---------------------------------------------------------------- which
+// With t tiles over the 256 CUs, of which a CU holds `fit` at once, and records
+// of 128 columns, a shape's time is taken as
+//   s + ceil(t / 256 fit) (e + c records) + (ceil(t / 256) w + t / 256 f) records
+// in us: what a round of workgroups takes alone, what those that share a CU
+// and those on other CUs add.  The numbers are least-squares fits (none
+// negative) of each shape's times at up to 189 sizes with groups of 128, 64 and
+// 32 (M from 1 to 8192, d x k of 9216 x 8192, 4096 x 4096, 5120 x 5120, 1024 x
+// 4096, 1024 x 1024, 1024 x 8192, 512 x 2048, 4096 x 512 and 8192 x 1024), good to
+// 3 - 12%; the choice takes 1.03 of the best of 25 shapes' time, on the mean.
+// The table holds those without which that gets worse by 0.1% or more.
+struct Cost {
+  int fit;
+  float s, e, c, w, f;
+};
+struct Shape {
+  int bm, bn;
+  bool rounds;  // the weights, to bf16
+  Cost cost[3];  // groups of 128 and more, 64, 32
+  void (*launch)(W4GemmArgs, hipStream_t);
+};
+template <int FM, int FN, int NW, int PD>
+constexpr Shape split(Cost g128, Cost g64, Cost g32) {
+  return {16 * FM, 16 * FN, false, {g128, g64, g32}, launch_split<FM, FN, NW, PD>};
+}
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS>
+constexpr Shape tile(Cost c) {
+  return {16 * FM * WM, 16 * FN * WN, true, {c, c, c}, launch_tile<FM, FN, WM, WN, KG, ST, WS>};
+}
+const Shape kShapes[] = {
+    split<1, 1, 8, 2>({1, 2.57f, 0.872f, 0.0337f, 0.f, 0.014f},
+                     {1, 2.6f, 0.93f, 0.0404f, 0.f, 0.0111f},
+                     {1, 2.45f, 0.988f, 0.0472f, 0.f, 0.0113f}),
+    split<1, 3, 8, 1>({2, 2.35f, 1.15f, 0.f, 0.0636f, 0.047f},
+                     {2, 2.f, 1.48f, 0.0035f, 0.0922f, 0.0322f},
+                     {2, 2.08f, 1.2f, 0.031f, 0.114f, 0.0278f}),
+    split<1, 2, 16, 1>({1, 2.32f, 1.16f, 0.0401f, 0.f, 0.0389f},
+                     {1, 2.17f, 1.25f, 0.0534f, 0.f, 0.034f},
+                     {1, 2.14f, 1.27f, 0.0779f, 0.f, 0.0333f}),
+    split<2, 2, 8, 1>({1, 2.7f, 0.671f, 0.0782f, 0.f, 0.0368f},
+                     {1, 2.6f, 0.75f, 0.0883f, 0.f, 0.0372f},
+                     {1, 2.74f, 0.711f, 0.136f, 0.f, 0.0148f}),
+    split<2, 3, 8, 1>({1, 2.51f, 0.831f, 0.118f, 0.f, 0.0413f},
+                     {1, 2.47f, 0.875f, 0.15f, 0.f, 0.0362f},
+                     {1, 1.54f, 1.88f, 0.192f, 0.f, 0.0617f}),
+    split<2, 4, 8, 1>({1, 1.63f, 1.7f, 0.139f, 0.f, 0.0604f},
+                     {1, 1.51f, 1.87f, 0.186f, 0.f, 0.0695f},
+                     {1, 1.58f, 2.04f, 0.253f, 0.f, 0.0595f}),
+    split<4, 3, 8, 1>({1, 1.09f, 3.03f, 0.186f, 0.f, 0.0754f},
+                     {1, 1.04f, 2.96f, 0.225f, 0.f, 0.0779f},
+                     {1, 1.28f, 3.18f, 0.317f, 0.f, 0.0752f}),
+    split<4, 4, 8, 1>({1, 1.34f, 3.2f, 0.27f, 0.f, 0.103f},
+                     {1, 1.48f, 3.12f, 0.295f, 0.f, 0.105f},
+                     {1, 1.37f, 3.57f, 0.396f, 0.f, 0.0956f}),
+    tile<4, 2, 1, 4, 2, 4, 2>({1, 1.48f, 2.4f, 0.582f, 0.f, 0.101f}),
+    tile<8, 2, 1, 4, 2, 3, 2>({1, 2.19f, 2.74f, 0.789f, 0.f, 0.242f}),
+    tile<4, 5, 2, 2, 2, 3, 2>({1, 1.97f, 3.25f, 1.17f, 0.f, 0.272f}),
+    tile<8, 2, 2, 4, 1, 4, 2>({1, 0.f, 5.06f, 1.51f, 0.f, 0.481f}),
+    tile<8, 3, 2, 4, 1, 3, 2>({1, 0.547f, 4.89f, 2.06f, 0.f, 0.547f}),
+    tile<8, 4, 2, 4, 1, 3, 2>({1, 0.f, 6.5f, 2.68f, 0.f, 0.733f}),
+};
+
+const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
+  const Shape *best = nullptr;
+  double least = 0;
+  for (const Shape &h : kShapes) {
+    const Cost &c = h.cost[sg >> 1];
+    const int64_t tiles = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
+    const double rounds = (double)((tiles + 256 * c.fit - 1) / (256 * c.fit)), cu = (double)((tiles + 255) / 256);
+    const double t = c.s + rounds * (c.e + (double)c.c * nb) + (cu * c.w + (double)tiles / 256 * c.f) * nb;
+    if (best == nullptr || t < least) {
+      best = &h;
+      least = t;
+    }
+  }
+  return *best;
+}
+
+// slabs whose grids stay far below what a launch takes
+constexpr int64_t kSlabM = int64_t(1) << 18, kSlabN = int64_t(1) << 20;
+
 }  // namespace
 
 hipError_t launch_w4_pack(const W4Args &a, hipStream_t st) {
@@ -158,28 +706,43 @@ hipError_t launch_w4_pack(const W4Args &a, hipStream_t st) {
 }
 
 hipError_t launch_w4_dequantize(const W4Args &a, hipStream_t st) {
-  const int64_t recs = (a.d + 15) / 16 * a.nb;
-  if (a.dtype == 1)
-    hipLaunchKernelGGL(k_w4_dequantize<uint16_t>, dim3((unsigned)recs), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL(k_w4_dequantize<float>, dim3((unsigned)recs), dim3(256), 0, st, a);
+  const int32_t per_row = (a.nb + kDqRecords - 1) / kDqRecords;
+  const dim3 grid((unsigned)((a.d + 15) / 16 * per_row));
+  if (a.dtype == 1) hipLaunchKernelGGL(k_w4_dequantize<uint16_t>, grid, dim3(256), 0, st, a, per_row);
+  else hipLaunchKernelGGL(k_w4_dequantize<float>, grid, dim3(256), 0, st, a, per_row);
   return hipGetLastError();
 }
 
+int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]) {
+  const Shape &s = best_of(std::min(M, kSlabM), std::min(d, kSlabN), (int32_t)((k + 127) / 128), sg);
+  out[0] = s.bm;
+  out[1] = s.bn;
+  out[2] = s.rounds;
+  return (int)(&s - kShapes);
+}
+
 hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st) {
-  constexpr int64_t kSlab = 16 * 65535;  // rows a launch
-  for (int64_t m0 = 0; m0 < all.M; m0 += kSlab) {
-    W4GemmArgs a = all;
-    a.M = (int32_t)std::min(kSlab, all.M - m0);
-    a.x += m0 * a.ldx;
-    a.y += m0 * a.ldy;
-    const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
-    if (a.sg == 1) hipLaunchKernelGGL(k_w4_rows<1>, grid, dim3(256), 0, st, a);
-    else if (a.sg == 2) hipLaunchKernelGGL(k_w4_rows<2>, grid, dim3(256), 0, st, a);
-    else hipLaunchKernelGGL(k_w4_rows<4>, grid, dim3(256), 0, st, a);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
+  // rows of x of a tile past 32-bit offsets of one another
+  const bool far = (uint64_t)256 * all.ldx * 2 + (uint64_t)all.K * 2 >= kOob;
+  for (int64_t m0 = 0; m0 < all.M; m0 += kSlabM)
+    for (int64_t n0 = 0; n0 < all.N; n0 += kSlabN) {
+      W4GemmArgs a = all;
+      a.M = (int32_t)std::min(kSlabM, all.M - m0);
+      a.N = (int32_t)std::min(kSlabN, all.N - n0);
+      a.x += m0 * a.ldx;
+      a.w += n0 / 16 * a.nb * w4_record(a.sg);
+      a.y += m0 * a.ldy + n0;
+      if (!far) {
+        best_of(a.M, a.N, a.nb, a.sg).launch(a, st);
+      } else {
+        const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
+        if (a.sg == 1) hipLaunchKernelGGL(k_w4_far<1>, grid, dim3(256), 0, st, a);
+        else if (a.sg == 2) hipLaunchKernelGGL(k_w4_far<2>, grid, dim3(256), 0, st, a);
+        else hipLaunchKernelGGL(k_w4_far<4>, grid, dim3(256), 0, st, a);
+      }
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   return hipSuccess;
 }
 

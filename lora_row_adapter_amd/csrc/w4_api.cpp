@@ -63,10 +63,7 @@ lora_status_t check_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int6
 }
 
 hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                       const lora_w4_t *W, void *y, int64_t ldy, void *ws, size_t ws_bytes,
-                       hipStream_t st) {
-  (void)ws;
-  (void)ws_bytes;
+                       const lora_w4_t *W, void *y, int64_t ldy, hipStream_t st) {
   W4GemmArgs a{};
   a.M = (int32_t)M;
   a.N = (int32_t)d;
@@ -138,29 +135,23 @@ lora_status_t lora_w4_dequantize(lora_dtype_t dtype, int64_t d, int64_t k, const
   return launch_w4_dequantize(a, (hipStream_t)stream) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
-size_t lora_gemm_w4_workspace_bytes(int64_t M, int64_t k, int64_t d) {
-  (void)M;
-  (void)k;
-  (void)d;
-  return 0;
+lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                           const lora_w4_t *W, void *y, int64_t ldy, void *stream) {
+  const lora_status_t s = check_gemm_w4(M, k, d, x, ldx, W, y, ldy, nullptr, 0);
+  if (s != LORA_OK || M == 0) return s;
+  const hipError_t e = timed(LORA_K_GEMM, (hipStream_t)stream,
+                             [&] { return run_gemm_w4(M, k, d, x, ldx, W, y, ldy, (hipStream_t)stream); });
+  return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
-lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                           const lora_w4_t *W, void *y, int64_t ldy, void *workspace,
-                           size_t workspace_bytes, void *stream) {
-  if (workspace != nullptr && workspace_bytes > 0 && (uintptr_t)workspace % 256 != 0) return LORA_ERR_WORKSPACE;
-  const lora_status_t s = check_gemm_w4(M, k, d, x, ldx, W, y, ldy, workspace, workspace_bytes);
-  if (s != LORA_OK || M == 0) return s;
-  const hipError_t e = timed(LORA_K_GEMM, (hipStream_t)stream, [&] {
-    return run_gemm_w4(M, k, d, x, ldx, W, y, ldy, workspace, workspace ? workspace_bytes : 0,
-                       (hipStream_t)stream);
-  });
-  return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+int32_t lora_test_gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t group, int32_t out[3]) {
+  if (out == nullptr || M < 1 || lora_w4_bytes(d, k, group) == 0) return -1;
+  return gemm_w4_shape(M, k, d, groups_in_record(group), out);
 }
 
 size_t lora_workspace_bytes_sliced_w4(int64_t max_rows, int64_t k, int32_t n_slices,
                                       const lora_slice_t *slices) {
-  if (k > kMaxK) return 0;
+  if (k < 1 || k > kMaxK) return 0;
   // the plan's regions alone, which depend on no type: in fp32 the dense base
   // product, which this layer does not run, takes none of its own
   return lora_workspace_bytes_sliced(max_rows, k, LORA_DTYPE_F32, n_slices, slices);

@@ -4,7 +4,7 @@ plain 64-bit implementations.
 Tolerances.  One rounding to bf16 is off by at most 2^-8 of the value.  A
 product rounds its fp32 sum once; w4_ref.sum_bound bounds that sum's error.
 Where x holds small whole numbers and scales are powers of two every sum is
-exact in fp32, in any order (|x| <= 4, 143 * 4 * k < 2^24), and so is every
+exact in fp32, in any order (|x| <= 4, 2 * 31 * 4 * k < 2^24), and so is every
 weight in bf16: the result is then the exact one rounded once, bit for bit.
 """
 import numpy as np
@@ -136,9 +136,33 @@ def test_product(M, k, d, group):
     xd, Wd = x.double().numpy(), R.dequant(q, s, z, group)
     want = xd @ Wd.T
     tol = 2.0 ** -8 * np.abs(want) + R.sum_bound(xd, s, z, group)
-    if lr.gemm_w4_workspace_bytes(M, k, d):  # each weight rounded once to bf16
+    if lr.test_gemm_w4_shape(M, k, d, group)[3]:  # each weight rounded once to bf16
         tol += 2.0 ** -8 * (np.abs(xd) @ np.abs(Wd).T)
     assert (np.abs(y - want) <= tol).all()
+
+
+# a size for every tile shape, its sizes odd and k past every ring of stages
+def one_for_each_shape():
+    found = {}
+    for M in (1, 3, 16, 30, 60, 100, 200, 300, 500, 800, 1100, 1500, 2100, 3000):
+        for d in (33, 300, 1000, 2050, 4100):
+            for k in (1032, 2056):
+                for group in (32, 64, 128):
+                    shape = lr.test_gemm_w4_shape(M, k, d, group)
+                    found.setdefault((shape[0], min(group, 128)), (M, k, d, group))
+    return found
+
+
+def test_every_tile_shape_exactly():
+    found = one_for_each_shape()
+    assert len({i for i, _ in found}) >= 12
+    for (i, _), (M, k, d, group) in sorted(found.items()):
+        say("w4 shape %d: %dx%dx%d g%d" % (i, M, d, k, group))
+        q, s, z = R.weight(M + d, d, k, group, exact=True)
+        x = whole(M, M, k)
+        y = lr.lora_gemm_w4(x.cuda(), device_weight(q, s, z, group))
+        want = (x.cuda().double() @ torch.from_numpy(R.dequant(q, s, z, group)).cuda().T).float().to(BF)
+        assert torch.equal(y, want)
 
 
 @pytest.mark.parametrize("M", [1, 4, 16, 40, 130, 700])
@@ -171,15 +195,19 @@ def test_product_of_far_rows():
     y = lr.lora_gemm_w4(view, W)
     want = torch.from_numpy(x.double().numpy() @ R.dequant(q, s, z, 64).T).float().to(BF)
     assert torch.equal(y.cpu(), want)
+    # and many rows of a stride just past a tile's 32-bit offsets
+    x = whole(6, 100, k)
+    view = far.as_strided((100, k), (1 << 23, 1))
+    view.copy_(x.cuda())
+    y = lr.lora_gemm_w4(view, W)
+    want = torch.from_numpy(x.double().numpy() @ R.dequant(q, s, z, 64).T).float().to(BF)
+    assert torch.equal(y.cpu(), want)
 
 
-def test_empty_batch_and_no_workspace():
+def test_empty_batch():
     q, s, z = R.weight(2, 20, 256, 128)
     W = device_weight(q, s, z, 128)
     assert lr.lora_gemm_w4(torch.empty(0, 256, dtype=BF, device="cuda"), W).shape == (0, 20)
-    x = whole(1, 9, 256).cuda()
-    none = torch.empty(0, dtype=torch.uint8, device="cuda")
-    assert torch.equal(lr.lora_gemm_w4(x, W, workspace=none), lr.lora_gemm_w4(x, W))
 
 
 @pytest.mark.parametrize("M", [1, 16, 50, 600])
@@ -308,7 +336,7 @@ def test_layer(case, pools):
     ids_d = torch.from_numpy(ids).cuda()
     ws = torch.zeros(lr.workspace_bytes_sliced_w4(M, k, slices), dtype=torch.uint8, device="cuda")
     want = layer_ref(x, R.dequant(q, s, z, group), ds, sets, ranks, scales.astype(np.float64), ids)
-    base = lr.lora_gemm_w4(x.cuda(), W, workspace=ws)
+    base = lr.lora_gemm_w4(x.cuda(), W)
     none = torch.from_numpy(np.flatnonzero(ids < 0)).cuda()
     for path in (lr.PATH_AUTO, lr.PATH_GATHER):
         y = lr.lora_linear_sliced_w4(x.cuda(), W, slices, ids_d, workspace=ws, path=path)
@@ -413,10 +441,9 @@ def test_captured_layer_replays(M):
     x, ids = loud(1, M, k).cuda(), torch.zeros(M, dtype=torch.int32, device="cuda")
     y, y0 = (torch.empty(M, sum(ds), dtype=BF, device="cuda") for _ in range(2))
     ws = torch.zeros(lr.workspace_bytes_sliced_w4(M, k, slices), dtype=torch.uint8, device="cuda")
-    gws = torch.empty(max(1, lr.gemm_w4_workspace_bytes(M, k, sum(ds))), dtype=torch.uint8, device="cuda")
 
     def go():
-        lr.lora_gemm_w4(x, W, y=y0, workspace=gws)
+        lr.lora_gemm_w4(x, W, y=y0)
         lr.lora_linear_sliced_w4(x, W, slices, ids, y=y, workspace=ws)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -470,9 +497,7 @@ def test_binding_refuses():
     x = torch.zeros(4, 256, dtype=BF, device="cuda")
     for args, kw in [((x.float(), W), {}), ((x[:, :128], W), {}), ((x.cpu(), W), {}),
                      ((x, W), dict(y=torch.empty(4, 31, dtype=BF, device="cuda"))),
-                     ((x, W), dict(y=torch.empty(4, 32, device="cuda"))),
-                     ((x, W), dict(workspace=torch.zeros(64, device="cuda"))),
-                     ((x, W), dict(workspace=torch.zeros(64, dtype=torch.uint8)))]:
+                     ((x, W), dict(y=torch.empty(4, 32, device="cuda")))]:
         with pytest.raises((TypeError, ValueError, lr.LoraError)):
             lr.lora_gemm_w4(*args, **kw)
     A, B = adapter_set(1, 2, 8, 256, 32, [8, 8])

@@ -61,8 +61,8 @@ def test_dequantize_refuses(want, kw, W):
     assert dequant(W, **kw) == want
 
 
-def gemm(W, M=4, k=256, d=16, x=1 << 26, ldx=256, y=1 << 28, ldy=16, ws=0, wsn=0):
-    return lr.load_library().lora_gemm_w4(M, k, d, x, ldx, ref(W), y, ldy, ws, wsn, None)
+def gemm(W, M=4, k=256, d=16, x=1 << 26, ldx=256, y=1 << 28, ldy=16):
+    return lr.load_library().lora_gemm_w4(M, k, d, x, ldx, ref(W), y, ldy, None)
 
 
 @pytest.mark.parametrize("want,kw,W", [
@@ -72,8 +72,6 @@ def gemm(W, M=4, k=256, d=16, x=1 << 26, ldx=256, y=1 << 28, ldy=16, ws=0, wsn=0
     (SHAPE, {"x": (1 << 26) + 8}, w4()), (SHAPE, {"k": 252}, w4()), (SHAPE, {"ldy": 15}, w4()),
     (SHAPE, {"y": (1 << 28) + 1}, w4()), (SHAPE, {"ldy": 1 << 40}, w4()),
     (ARG, {"y": (1 << 26) + 512}, w4()), (ARG, {"y": 1 << 24}, w4()),
-    (WORKSPACE, {"ws": (1 << 30) + 8, "wsn": 512}, w4()), (ARG, {"ws": 1 << 28, "wsn": 512}, w4()),
-    (ARG, {"ws": 1 << 24, "wsn": 512}, w4()), (ARG, {"ws": 1 << 26, "wsn": 512}, w4()),
     (0, {"M": 0, "x": 0, "y": 0}, w4()),
 ])
 def test_gemm_refuses(want, kw, W):
@@ -105,6 +103,16 @@ def layer(W="w", M=4, k=256, x=1 << 26, ldx=256, sl=None, n=1, ids=1 << 14, y=1 
 ])
 def test_layer_refuses(want, kw):
     assert layer(**kw) == want
+
+
+def test_shape_hook():
+    lib = lr.load_library()
+    out = (ctypes.c_int32 * 3)()
+    assert lib.lora_test_gemm_w4_shape(1, 8192, 9216, 128, out) >= 0 and out[0] == 16 and out[2] == 0
+    assert lib.lora_test_gemm_w4_shape(8192, 4096, 4096, 64, out) >= 0 and out[0] >= 128 and out[2] == 1
+    for M, k, d, group, o in [(0, 64, 64, 32, out), (1, 0, 64, 32, out), (1, 64, 0, 32, out), (1, 64, 64, 31, out),
+                              (1, 64, 64, 32, None)]:
+        assert lib.lora_test_gemm_w4_shape(M, k, d, group, o) == -1
 
 
 def test_workspace_sizes():

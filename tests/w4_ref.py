@@ -42,12 +42,12 @@ def kept(s):
 
 def sum_bound(x, s, z, group):
     """Bound of the fp32 part of a product's error: a group of at most 128
-    columns is a sum of products with 128 + q (at most 143) and one of x times
-    128 + z (at most 159); 2^-23 of the magnitudes for each of 128 additions,
-    and as much again for the groups' sums."""
+    columns is a sum of products with codes (at most 15) and one of x times a
+    zero point (at most 31); 2^-23 of the magnitudes for each of 128 additions,
+    and as much again for the groups' sums (fewer than 128 of them)."""
     k = x.shape[1]
     rep = np.repeat(np.abs(s.double().numpy()), group, 1)[:, :k]
-    return 2 * 128 * 2.0 ** -23 * (143 + 159) * (np.abs(x) @ rep.T)
+    return 2 * 128 * 2.0 ** -23 * (15 + 31) * (np.abs(x) @ rep.T)
 
 
 def heads(x, w, eps, cos, sin, rot, interleaved):
