@@ -1216,8 +1216,10 @@ def lora_gemm_w4(x: torch.Tensor, W: W4, y: Optional[torch.Tensor] = None,
     if W.k != k or W.device != device:
         raise ValueError("x and W differ in k or device")
     if y is None:
-        y = _empty((M, W.d), bf, device, stream)
-        yp, ldy = y.data_ptr(), W.d
+        ldy = W.d
+        y = (torch.empty_strided((M, ldy), (ldy, 1), dtype=bf, device=device) if stream is None
+             else _empty((M, ldy), bf, device, stream))
+        yp = y.data_ptr()
     else:
         yp, ldy = _matrix(y, "y", (M, W.d), bf, device)
     _on(device, stream, lib.lora_gemm_w4, "lora_gemm_w4", M, k, W.d, xp, ldx, W._ref, yp, ldy)
@@ -1279,34 +1281,48 @@ class Rope:
     in radians a position, pairs (i, i + rot_dim / 2) or, interleaved, (2i,
     2i + 1), and a factor on cos and sin."""
 
-    __slots__ = ("inv_freq", "rot_dim", "interleaved", "scale")
+    __slots__ = ("inv_freq", "rot_dim", "interleaved", "scale", "device", "pointer")
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
-        _dev(inv_freq, "inv_freq", torch.float32)
+        self.pointer, self.device = _dev(inv_freq, "inv_freq", torch.float32), inv_freq.device
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be 1-D")
         self.inv_freq, self.rot_dim = inv_freq, 2 * inv_freq.numel()
         self.interleaved, self.scale = bool(interleaved), float(scale)
 
 
-def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, device) -> _CHeads:
-    if x.dtype is not dtype or out.dtype is not dtype or weight is not None and weight.dtype is not dtype:
-        raise TypeError("%s, its weight and its output must share q's dtype" % name)
-    if x.device != device or out.device != device or weight is not None and weight.device != device:
-        raise ValueError("%s, its weight and its output must be on q's device" % name)
+def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, device, stream):
+    """(descriptor, output) of the heads of q or k, whose own type and device
+    have been checked."""
     M, H, D = shape
-    if out.shape != shape:
-        raise ValueError("%s's output must be [%d, %d, %d]" % (name, M, H, D))
     lr, lh, unit = x.stride()
-    lor, loh, ounit = out.stride()
-    if D > 1 and (unit != 1 or ounit != 1):
-        raise ValueError("%s and its output must have unit stride along their last dimension" % name)
-    wp = None
-    if weight is not None:
-        if weight.shape != (D,) or not weight.is_contiguous():
-            raise ValueError("%s's weight must be a contiguous [%d] tensor" % (name, D))
+    if unit != 1 and D > 1:
+        raise ValueError("%s must have unit stride along its last dimension" % name)
+    if weight is None:
+        wp = None
+    else:
+        if weight.dtype is not dtype:
+            raise TypeError("%s's weight must share its dtype" % name)
+        if weight.device != device or weight.shape != shape[2:] or not weight.is_contiguous():
+            raise ValueError("%s's weight must be a contiguous [%d] tensor on its device" % (name, D))
         wp = weight.data_ptr()
-    return _CHeads(H, x.data_ptr(), lr, lh, wp, out.data_ptr(), lor, loh)
+    if out is None:
+        lor, loh = H * D, D
+        # (by strides: 1.3 us a call against torch.empty's 2.1)
+        out = (torch.empty_strided(shape, (lor, loh, 1), dtype=dtype, device=device) if stream is None
+               else _empty(shape, dtype, device, stream))
+    else:
+        if out.dtype is not dtype:
+            raise TypeError("%s's output must share its dtype" % name)
+        if out.device != device or out.shape != shape:
+            raise ValueError("%s's output must be [%d, %d, %d] on its device" % (name, M, H, D))
+        lor, loh, unit = out.stride()
+        if unit != 1 and D > 1:
+            raise ValueError("%s's output must have unit stride along its last dimension" % name)
+    return _CHeads(H, x.data_ptr(), lr, lh, wp, out.data_ptr(), lor, loh), out
+
+
+_byref = ctypes.byref
 
 
 def lora_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
@@ -1319,35 +1335,34 @@ def lora_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     two outputs.  q_out and k_out may be q and k themselves.  Rows with a
     negative position are left as they are: of outputs made here, unset."""
     lib = _lib or load_library()
-    dtype, device = q.dtype, q.device
+    dtype, device, shape = q.dtype, q.device, q.shape
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
-    if q.dim() != 3 or not q.is_cuda:
+    if len(shape) != 3 or device.type != "cuda":
         raise ValueError("q must be a 3-D device tensor")
-    M, _, D = shape = q.shape
-    if q_out is None:
-        q_out = _empty(shape, dtype, device, stream)
-    cq = _head_set(q, "q", q_weight, q_out, shape, dtype, device)
-    ck = None
+    M, _, D = shape
+    cq, q_out = _head_set(q, "q", q_weight, q_out, shape, dtype, device, stream)
+    ck = cr = None
     if k is not None:
-        if k.dim() != 3 or k.shape[0] != M or k.shape[2] != D:
-            raise ValueError("k must be [%d, heads, %d]" % (M, D))
-        if k_out is None:
-            k_out = _empty(k.shape, dtype, device, stream)
-        ck = ctypes.byref(_head_set(k, "k", k_weight, k_out, k.shape, dtype, device))
-    cr = None
+        ks = k.shape
+        if len(ks) != 3 or ks[0] != M or ks[2] != D or k.device != device:
+            raise ValueError("k must be [%d, heads, %d] on q's device" % (M, D))
+        if k.dtype is not dtype:
+            raise TypeError("k must share q's dtype")
+        ck, k_out = _head_set(k, "k", k_weight, k_out, ks, dtype, device, stream)
+        ck = _byref(ck)
     if rope is not None:
         if positions is None:
             raise ValueError("a rotation needs positions")
         if positions.dtype is not torch.int64:
             raise TypeError("positions must be int64")
-        if positions.shape != (M,) or positions.device != device or not positions.is_contiguous():
+        if positions.shape != shape[:1] or positions.device != device or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous [%d] tensor on q's device" % M)
-        _same_device(rope.inv_freq, "inv_freq", device)
-        cr = ctypes.byref(_CRope(positions.data_ptr(), rope.inv_freq.data_ptr(), rope.rot_dim,
-                                 rope.interleaved, rope.scale))
-    _on(device, stream, lib.lora_qk_norm_rope, "lora_qk_norm_rope", dt, M, D, eps, ctypes.byref(cq), ck, cr)
+        if rope.device != device:
+            raise ValueError("inv_freq must be a tensor on q's device")
+        cr = _byref(_CRope(positions.data_ptr(), rope.pointer, rope.rot_dim, rope.interleaved, rope.scale))
+    _on(device, stream, lib.lora_qk_norm_rope, "lora_qk_norm_rope", dt, M, D, eps, _byref(cq), ck, cr)
     return q_out, k_out
 
 

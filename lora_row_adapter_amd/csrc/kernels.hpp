@@ -277,6 +277,10 @@ struct HeadsArgs {
   HeadSet s[2];
   const int64_t *pos;      // nullptr: no rotation
   const float *inv_freq;
+  // filled in by launch_heads
+  int32_t lanes;       // log2 of the lanes that share a head
+  uint32_t per_block;  // heads of a workgroup
+  double inv_d;
 };
 hipError_t launch_heads(const HeadsArgs &a, hipStream_t st);
 hipError_t launch_shrink_gather(const LoraArgs &a, hipStream_t st);
