@@ -18,7 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "liblora_row.so")
 SOURCES = ["lora_api.cpp", "plan.hip", "gemm.hip", "lora_gather.hip", "lora_sgmv.hip",
            "pool.hip", "pool_mgr.cpp", "merge.hip", "gemm_q.hip", "noalloc.hip",
-           "mx.hip", "gemm_mx.hip", "mx_api.cpp", "w4.hip", "w4_api.cpp", "heads.hip",
+           "mx.hip", "gemm_mx.hip", "mx_api.cpp", "w4.hip", "w4_layer.hip", "w4_api.cpp", "heads.hip",
            "heads_api.cpp"]
 ARCH = os.environ.get("LORA_ROW_ARCH", "gfx950")
 

@@ -258,7 +258,33 @@ struct W4GemmArgs {
   int64_t ldy;
   int32_t tiles_m, tiles_n;
 };
-hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st);
+// The layer for at most kW4Rows rows, without a plan: launch_w4_shrink checks
+// the rows (row[], the counts in hdr) and writes t = scale_s x A_s^T of each
+// row's own adapter s, as two bf16 whose sum keeps 16 bits, and the product adds
+// t B_s^T to its sums.
+constexpr int kW4Rows = 64;
+struct W4Lora {
+  int32_t n_slices, S, M;
+  int32_t Rp;               // rows of t: max rank over slices rounded up to 32
+  SliceRef sl[kMaxSlices];
+  int64_t n_pages[kMaxSlices];
+  const int32_t *ids;
+  int32_t *hdr;             // counts of bad ids, ranks, pages (HdrWord)
+  int32_t *row;             // [M]: the adapter to apply, or -1
+  uint16_t *t_hi, *t_lo;    // [n_slices, M, Rp]
+  const uint16_t *x;
+  int64_t ldx, k;
+};
+hipError_t launch_w4_shrink(const W4Lora &a, hipStream_t st);
+// Bytes of row[] and t.
+size_t w4_lora_bytes(int64_t M, int32_t n_slices, int32_t R);
+// plan: run it in this launch, in a workgroup beside the tiles (only where
+// gemm_w4_runs_plan says so); lora: add this (at most kW4Rows rows that
+// gemm_w4_adds_lora accepts).
+hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st, const PlanArgs *plan = nullptr,
+                          const W4Lora *lora = nullptr);
+bool gemm_w4_runs_plan(const W4GemmArgs &a);
+bool gemm_w4_adds_lora(const W4GemmArgs &a);
 // Index of the tile shape it takes; out: its rows, columns and whether it rounds
 // the weights to bf16.
 int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]);
@@ -371,8 +397,8 @@ struct W4Base {
 lora_status_t check_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
                             const lora_w4_t *W, const void *y, int64_t ldy, const void *workspace,
                             size_t workspace_bytes);
-hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                       const lora_w4_t *W, void *y, int64_t ldy, hipStream_t st);
+W4GemmArgs make_w4_args(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                        const lora_w4_t *W, void *y, int64_t ldy);
 // Optional per-kernel timing (lora_profile_*; defined in lora_api.cpp).
 namespace prof {
 int begin(int c, hipStream_t st);

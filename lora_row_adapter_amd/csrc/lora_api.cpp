@@ -534,6 +534,37 @@ static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d
   return launch_gemm_mx(g, st);
 }
 
+// The 4-bit layer for a few rows: two launches and no plan (the workspace's
+// plan regions stay as they are).
+static lora_status_t run_w4_rows(const LoraArgs &a, const W4GemmArgs &g, const WsLayout &L, int32_t S,
+                                 const lora_slice_t *slices, const int32_t *ids, hipStream_t st) {
+  W4Lora l{};
+  l.n_slices = a.n_slices;
+  l.S = S;
+  l.M = g.M;
+  l.Rp = (a.R + 31) & ~31;
+  for (int q = 0; q < a.n_slices; ++q) {
+    l.sl[q] = a.sl[q];
+    l.n_pages[q] = slices[q].adapters.n_pages;
+  }
+  l.ids = ids;
+  l.hdr = reinterpret_cast<int32_t *>(a.ws + L.hdr);
+  // in the place of the shrink's partials, which are 16 times as many
+  uint8_t *at = a.ws + L.tpart;
+  const size_t t = (size_t)a.n_slices * g.M * l.Rp * sizeof(uint16_t);
+  l.t_hi = reinterpret_cast<uint16_t *>(at);
+  l.t_lo = reinterpret_cast<uint16_t *>(at + t);
+  l.row = reinterpret_cast<int32_t *>(at + 2 * t);
+  if (L.tpart + w4_lora_bytes(g.M, a.n_slices, a.R) > L.total) return LORA_ERR_WORKSPACE;
+  l.x = g.x;
+  l.ldx = g.ldx;
+  l.k = g.K;
+  hipError_t e = timed(LORA_K_SGMV_SHRINK, st, [&] { return launch_w4_shrink(l, st); });
+  if (e != hipSuccess) return LORA_ERR_HIP;
+  e = timed(LORA_K_GEMM, st, [&] { return launch_gemm_w4(g, st, nullptr, &l); });
+  return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
+}
+
 // The layer over several slices; the base weight is dense (W, ldw) or, with
 // qw != nullptr, quantized, with mx != nullptr microscaled or with w4 !=
 // nullptr 4-bit (all bf16 only).  self_contained: use no library
@@ -603,6 +634,11 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
     sr.d = slices[q].d;
     sr.col0 = col0;
     col0 += slices[q].d;
+  }
+
+  if (w4 && M <= kW4Rows && path != LORA_PATH_GATHER) {
+    const W4GemmArgs g = make_w4_args(M, k, d_total, x, ldx, w4->W, y, ldy);
+    if (gemm_w4_adds_lora(g)) return run_w4_rows(a, g, ws_layout(M, S, R, n_slices), S, slices, adapter_ids, st);
   }
 
   for (int64_t c0 = 0; c0 < M; c0 += kPlanMaxRows) {
@@ -718,9 +754,13 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                          gemm_runs_plan(dtype, Mc, k, d_total, ldx, ldw, gws, gws_bytes, fcap > 0);
     // and so does a microscaled layer's first launch, the norm or quantising
     const bool in_prep = !reuse && mx && mx_runs_plan(Mc, k, S, mx->norm != nullptr);
+    // and a 4-bit product; where that has no room for it, the plan goes ahead
+    // on the same stream, as the fork and join take longer than it
+    const W4GemmArgs g4 = w4 ? make_w4_args(Mc, k, d_total, xc, ldx, w4->W, yc, ldy) : W4GemmArgs{};
+    const bool in_w4 = !reuse && w4 && gemm_w4_runs_plan(g4);
     PlanArgs gplan{};
-    if (in_gemm || in_prep) gplan = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
-    bool beside = !self_contained && !in_gemm && !in_prep;
+    if (in_gemm || in_prep || in_w4) gplan = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
+    bool beside = !self_contained && !in_gemm && !in_prep && !w4;
     if (!reuse && dense && beside) {
       KernelFootprint pf, gf;
       const PlanArgs pa = make_plan_args(Mc, k, dtype, n_slices, slices, adapter_ids + c0, ws, L);
@@ -729,7 +769,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
                fits_beside(gf, pf);
     }
     const bool fork = !reuse && beside && !self_contained && side::get(&ps, &ev_fork, &ev_join);
-    if (!reuse && !in_gemm && !in_prep) {
+    if (!reuse && !in_gemm && !in_prep && !in_w4) {
       if (fork) {
         if (hipEventRecord(ev_fork, st) != hipSuccess || hipStreamWaitEvent(ps, ev_fork, 0) != hipSuccess)
           return LORA_ERR_HIP;
@@ -743,7 +783,7 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
       if (mx)
         return run_mx_base(*mx, Mc, k, d_total, c0, xc, ldx, yc, ldy, ws + L.total, XL,
                            in_prep ? &gplan : nullptr, st);
-      if (w4) return run_gemm_w4(Mc, k, d_total, xc, ldx, w4->W, yc, ldy, st);
+      if (w4) return launch_gemm_w4(g4, st, in_w4 ? &gplan : nullptr);
       if (qw) return launch_gemm_q(make_q_args(qw, Mc, k, d_total, xc, ldx, yc, ldy), st);
       // expired split-K waits are counted in the plan header, where
       // lora_check reads them

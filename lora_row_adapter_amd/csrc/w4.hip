@@ -10,8 +10,9 @@
 //   tot += s (acc - z X)
 // in fp32: no weight is rounded.
 #include <algorithm>
+#include <type_traits>
 
-#include "kernels.hpp"
+#include "plan_body.hpp"
 
 namespace lora {
 
@@ -165,16 +166,106 @@ __device__ __forceinline__ void read_half(uint32_t a0, uint32_t a1, u32x4_t (&x)
 // both PD records ahead.  The waves' sums meet in LDS at the end, in their order.
 // Loads past the end of a wave's records, of x's rows and of its columns are
 // past their buffer: they move nothing and give zeros.
-template <int FM, int FN, int NW, int PD, int SG>
-__global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p) {
+// kWith: kPlan: workgroup 0 runs the layer's plan; kLora: the adapters' part is
+// added (see add_lora).
+enum With { kNone, kPlan, kLora };
+struct Nothing {};
+template <With kWith>
+using with_t = std::conditional_t<kWith == kPlan, PlanArgs, std::conditional_t<kWith == kLora, W4Lora, Nothing>>;
+
+// B_s[n][j .. j + 7] of slice q, zeros from the rank r on.
+__device__ __forceinline__ bf16x8_t load_b(const SliceRef &sl, int s, int r, int64_t n, int j) {
+  u32x4_t v = {0, 0, 0, 0};
+  if (j < r) {
+    const int stride = sl.ar.pooled ? r : sl.ar.max_rank;  // of B's rows
+    if (stride % 8 == 0) {  // whole vectors, of one page
+      v = *reinterpret_cast<const u32x4_t *>(adapter_b_ptr(sl.ar, s, r, n, j));
+      if (r - j < 8) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (2 * e >= r - j) v[e] = 0;
+          else if (2 * e + 1 >= r - j) v[e] &= 0xFFFFu;
+        }
+      }
+    } else {
+      for (int e = 0; e < 8 && j + e < r; ++e)
+        v[e >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(adapter_b_ptr(sl.ar, s, r, n, j + e)) << (16 * (e & 1));
+    }
+  }
+  return __builtin_bit_cast(bf16x8_t, v);
+}
+
+// Adds t B_s^T to the sums of this workgroup's rows, each distinct adapter and
+// 16 columns the work of one of its waves.  A product is taken for all 16 rows of
+// a tile and added to those of that adapter alone, so no adapter's values reach
+// another's rows.
+template <int FM, int FN, int NW>
+__device__ __forceinline__ void add_lora(const W4Lora &l, int m0, int n0, int N, int wave,
+                                         f32x4_t (&tot)[FM][FN]) {
+  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  const int own = lane < 16 * FM && m0 + lane < l.M ? l.row[m0 + lane] : -1;  // of row m0 + lane
+  uint64_t left = __ballot(own >= 0);
+  for (int c = 0; left != 0; c += FN) {
+    const int s = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
+    const uint64_t mine = __ballot(own == s);
+    left &= ~mine;
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      if ((c + j) % NW != wave) continue;
+      const int n = n0 + 16 * j + r;
+      for (int q = 0; q < l.n_slices; ++q) {
+        const SliceRef &sl = l.sl[q];
+        const int64_t at = n - sl.col0;
+        if (n0 + 16 * j + 15 < sl.col0 || n0 + 16 * j >= sl.col0 + sl.d) continue;
+        const int rank = sl.ranks[s], full = (rank + 15) & ~15;  // t is written up to there
+        const bool in = n < N && at >= 0 && at < sl.d;
+        f32x4_t acc[FM];
+#pragma unroll
+        for (int m = 0; m < FM; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int k0 = 0; k0 < rank; k0 += 32) {
+          const int k = k0 + 8 * h;
+          const bf16x8_t b = load_b(sl, s, in ? rank : 0, in ? at : 0, k);
+#pragma unroll
+          for (int m = 0; m < FM; ++m) {
+            u32x4_t hi = {0, 0, 0, 0}, lo = hi;
+            if (k < full && (mine >> (16 * m + r) & 1)) {
+              const int64_t o = ((int64_t)q * l.M + m0 + 16 * m + r) * l.Rp + k;
+              hi = *reinterpret_cast<const u32x4_t *>(l.t_hi + o);
+              lo = *reinterpret_cast<const u32x4_t *>(l.t_lo + o);
+            }
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), b, acc[m], 0, 0, 0);
+            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, lo), b, acc[m], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int m = 0; m < FM; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (in && (mine >> (16 * m + 4 * h + e) & 1)) tot[m][j][e] += acc[m][e];
+      }
+    }
+  }
+}
+
+template <int FM, int FN, int NW, int PD, int SG, With kWith>
+__global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p, with_t<kWith> with) {
   constexpr int REC = (int)w4_record(SG), KS = 4 / SG;
   constexpr int HALF = FM * 2048, XI = 2 * FM;  // x: bytes of half a record, loads of 1 KiB
   constexpr int RING = NW * PD * 2 * HALF, PART = NW * FM * FN * 1024;
   constexpr int kYounger = XI + (PD - 1) * (FN * (1 + SG) + 2 * XI) + FN * (1 + SG);
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max(RING, PART)];
+  constexpr int PLAN = kWith == kPlan ? (int)plan_detail::plan_sort_lds(plan_detail::kPlanRowBitsMax) : 0;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max({RING, PART, PLAN})];
+  int bx = blockIdx.x;
+  if constexpr (kWith == kPlan) {
+    if (bx == 0) {
+      if (blockIdx.y == 0) plan_detail::plan_body<64 * NW>(with, smem, sizeof(smem));
+      return;
+    }
+    --bx;
+  }
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * (16 * FN), m0 = blockIdx.y * (16 * FM);
+  const int n0 = bx * (16 * FN), m0 = blockIdx.y * (16 * FM);
   const int mr = min(16 * FM, p.M - m0), nr = min(16 * FN, p.N - n0);
   const uint32_t tile_bytes = (uint32_t)p.nb * REC;
   const auto rx = rsrc(p.x + (int64_t)m0 * p.ldx, (uint32_t)(((mr - 1) * p.ldx + p.K) * 2));
@@ -219,6 +310,10 @@ __global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p) {
     asm volatile("" ::: "memory");
     load_x(d, d, 0);
     load_x(d, d, 1);
+    asm volatile("" ::: "memory");
+  }
+  if constexpr (kWith == kLora) {  // while the first records are on their way
+    add_lora<FM, FN, NW>(with, m0, n0, p.N, wave, tot);
     asm volatile("" ::: "memory");
   }
   for (int t0 = 0; t0 < cnt; t0 += PD) {
@@ -294,12 +389,24 @@ __global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p) {
   }
 }
 
+// What goes with a launch: nothing, a plan or the adapters' part.
+struct Extra {
+  const PlanArgs *plan;
+  const W4Lora *lora;
+};
+
+template <int FM, int FN, int NW, int PD, int SG>
+void launch_split(const W4GemmArgs &a, const Extra &x, hipStream_t st) {
+  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN) + (x.plan ? 1 : 0), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
+  if (x.plan) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kPlan>), grid, block, 0, st, a, *x.plan);
+  else if (x.lora) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kLora>), grid, block, 0, st, a, *x.lora);
+  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kNone>), grid, block, 0, st, a, Nothing{});
+}
 template <int FM, int FN, int NW, int PD>
-void launch_split(W4GemmArgs a, hipStream_t st) {
-  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
-  if (a.sg == 1) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 1>), grid, block, 0, st, a);
-  else if (a.sg == 2) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 2>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 4>), grid, block, 0, st, a);
+void launch_split(W4GemmArgs a, const Extra &x, hipStream_t st) {
+  if (a.sg == 1) launch_split<FM, FN, NW, PD, 1>(a, x, st);
+  else if (a.sg == 2) launch_split<FM, FN, NW, PD, 2>(a, x, st);
+  else launch_split<FM, FN, NW, PD, 4>(a, x, st);
 }
 
 // Rows of x past 32-bit offsets of one another (the last tokens of long
@@ -415,8 +522,8 @@ struct WTile {
 
 // The tile of this workgroup: each XCD takes a contiguous run of tiles, bands
 // of eight row tiles down, then across.
-__device__ __forceinline__ void tile_of(const W4GemmArgs &p, int &tm, int &tn) {
-  const uint32_t nblk = (uint32_t)p.tiles_m * p.tiles_n, b = blockIdx.x;
+__device__ __forceinline__ void tile_of(const W4GemmArgs &p, uint32_t b, int &tm, int &tn) {
+  const uint32_t nblk = (uint32_t)p.tiles_m * p.tiles_n;
   const uint32_t xcd = b & 7, each = nblk >> 3, more = nblk & 7;
   const uint32_t t = xcd * each + (xcd < more ? xcd : more) + (b >> 3);
   const uint32_t band = t / (8u * p.tiles_n), in = t - band * 8u * p.tiles_n;
@@ -425,13 +532,22 @@ __device__ __forceinline__ void tile_of(const W4GemmArgs &p, int &tm, int &tn) {
   tn = (int)(in / rows_in);
 }
 
-template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG>
-__global__ __launch_bounds__(64 * WM * WN * KG) void k_w4_tile(W4GemmArgs p) {
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG, With kWith>
+__global__ __launch_bounds__(64 * WM * WN * KG) void k_w4_tile(W4GemmArgs p, with_t<kWith> with) {
   using T = WTile<FM, FN, WM, WN, KG, ST, WS, SG>;
   constexpr int BM = T::BM, BN = T::BN, REC = (int)w4_record(SG);
+  static_assert(T::SMEM >= plan_detail::plan_sort_lds(plan_detail::kPlanRowBitsMax), "room for the plan");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[T::SMEM];
+  uint32_t b = blockIdx.x;
+  if constexpr (kWith == kPlan) {
+    if (b == 0) {
+      plan_detail::plan_body<T::NT>(with, smem, sizeof(smem));
+      return;
+    }
+    --b;
+  }
   int tm, tn;
-  tile_of(p, tm, tn);
+  tile_of(p, b, tm, tn);
   const int m0 = tm * BM, n0 = tn * BN;
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -605,15 +721,20 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4_tile(W4GemmArgs p) {
   }
 }
 
+template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG>
+void launch_tile(const W4GemmArgs &a, const Extra &x, hipStream_t st) {
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n) + (x.plan ? 1 : 0)), block(64 * WM * WN * KG);
+  if (x.plan) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, SG, kPlan>), grid, block, 0, st, a, *x.plan);
+  else hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, SG, kNone>), grid, block, 0, st, a, Nothing{});
+}
 template <int FM, int FN, int WM, int WN, int KG, int ST, int WS>
-void launch_tile(W4GemmArgs a, hipStream_t st) {
+void launch_tile(W4GemmArgs a, const Extra &x, hipStream_t st) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n)), block(64 * WM * WN * KG);
-  if (a.sg == 1) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 1>), grid, block, 0, st, a);
-  else if (a.sg == 2) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 2>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, 4>), grid, block, 0, st, a);
+  if (a.sg == 1) launch_tile<FM, FN, WM, WN, KG, ST, WS, 1>(a, x, st);
+  else if (a.sg == 2) launch_tile<FM, FN, WM, WN, KG, ST, WS, 2>(a, x, st);
+  else launch_tile<FM, FN, WM, WN, KG, ST, WS, 4>(a, x, st);
 }
 
 // ---------------------------------------------------------------- which
@@ -634,16 +755,20 @@ struct Cost {
 struct Shape {
   int bm, bn;
   bool rounds;  // the weights, to bf16
+  int held;      // workgroups that a CU holds
   Cost cost[3];  // groups of 128 and more, 64, 32
-  void (*launch)(W4GemmArgs, hipStream_t);
+  void (*launch)(W4GemmArgs, const Extra &, hipStream_t);
 };
+constexpr int held(int smem, int waves) { return std::max(1, std::min(160 * 1024 / smem, 16 / waves)); }
 template <int FM, int FN, int NW, int PD>
 constexpr Shape split(Cost g128, Cost g64, Cost g32) {
-  return {16 * FM, 16 * FN, false, {g128, g64, g32}, launch_split<FM, FN, NW, PD>};
+  return {16 * FM, 16 * FN, false, held(std::max(NW * PD * FM * 4096, NW * FM * FN * 1024), NW),
+          {g128, g64, g32}, launch_split<FM, FN, NW, PD>};
 }
 template <int FM, int FN, int WM, int WN, int KG, int ST, int WS>
 constexpr Shape tile(Cost c) {
-  return {16 * FM * WM, 16 * FN * WN, true, {c, c, c}, launch_tile<FM, FN, WM, WN, KG, ST, WS>};
+  return {16 * FM * WM, 16 * FN * WN, true, held(WTile<FM, FN, WM, WN, KG, ST, WS, 1>::SMEM, WM * WN * KG),
+          {c, c, c}, launch_tile<FM, FN, WM, WN, KG, ST, WS>};
 }
 const Shape kShapes[] = {
     split<1, 1, 8, 2>({1, 2.57f, 0.872f, 0.0337f, 0.f, 0.014f},
@@ -682,6 +807,7 @@ const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
   const Shape *best = nullptr;
   double least = 0;
   for (const Shape &h : kShapes) {
+    if (h.rounds && M <= kW4Rows) continue;  // the adapters' part goes with the others
     const Cost &c = h.cost[sg >> 1];
     const int64_t tiles = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
     const double rounds = (double)((tiles + 256 * c.fit - 1) / (256 * c.fit)), cu = (double)((tiles + 255) / 256);
@@ -721,9 +847,23 @@ int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]) {
   return (int)(&s - kShapes);
 }
 
-hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st) {
-  // rows of x of a tile past 32-bit offsets of one another
-  const bool far = (uint64_t)256 * all.ldx * 2 + (uint64_t)all.K * 2 >= kOob;
+// rows of x of a tile past 32-bit offsets of one another
+static bool far_rows(const W4GemmArgs &a) { return (uint64_t)256 * a.ldx * 2 + (uint64_t)a.K * 2 >= kOob; }
+
+bool gemm_w4_adds_lora(const W4GemmArgs &a) { return a.M <= kW4Rows && a.N <= kSlabN && !far_rows(a); }
+
+// Where the CUs are not all full of tiles to the last, a plan costs no more than
+// its own time.
+bool gemm_w4_runs_plan(const W4GemmArgs &a) {
+  if (a.M > kPlanMaxRows || a.N > kSlabN || far_rows(a)) return false;
+  const Shape &h = best_of(a.M, a.N, a.nb, a.sg);
+  const int64_t tiles = (int64_t)((a.M + h.bm - 1) / h.bm) * ((a.N + h.bn - 1) / h.bn);
+  return tiles % (256 * h.held) != 0;
+}
+
+hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs *plan, const W4Lora *lora) {
+  const bool far = far_rows(all);
+  if ((plan && !gemm_w4_runs_plan(all)) || (lora && !gemm_w4_adds_lora(all))) return hipErrorInvalidValue;
   for (int64_t m0 = 0; m0 < all.M; m0 += kSlabM)
     for (int64_t n0 = 0; n0 < all.N; n0 += kSlabN) {
       W4GemmArgs a = all;
@@ -733,7 +873,7 @@ hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st) {
       a.w += n0 / 16 * a.nb * w4_record(a.sg);
       a.y += m0 * a.ldy + n0;
       if (!far) {
-        best_of(a.M, a.N, a.nb, a.sg).launch(a, st);
+        best_of(a.M, a.N, a.nb, a.sg).launch(a, Extra{plan, lora}, st);
       } else {
         const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
         if (a.sg == 1) hipLaunchKernelGGL(k_w4_far<1>, grid, dim3(256), 0, st, a);

@@ -62,8 +62,8 @@ lora_status_t check_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int6
   return LORA_OK;
 }
 
-hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
-                       const lora_w4_t *W, void *y, int64_t ldy, hipStream_t st) {
+W4GemmArgs make_w4_args(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
+                        const lora_w4_t *W, void *y, int64_t ldy) {
   W4GemmArgs a{};
   a.M = (int32_t)M;
   a.N = (int32_t)d;
@@ -75,7 +75,7 @@ hipError_t run_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t l
   a.w = (const uint8_t *)W->data;
   a.y = (uint16_t *)y;
   a.ldy = ldy;
-  return launch_gemm_w4(a, st);
+  return a;
 }
 
 }  // namespace lora
@@ -140,7 +140,7 @@ lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64
   const lora_status_t s = check_gemm_w4(M, k, d, x, ldx, W, y, ldy, nullptr, 0);
   if (s != LORA_OK || M == 0) return s;
   const hipError_t e = timed(LORA_K_GEMM, (hipStream_t)stream,
-                             [&] { return run_gemm_w4(M, k, d, x, ldx, W, y, ldy, (hipStream_t)stream); });
+                             [&] { return launch_gemm_w4(make_w4_args(M, k, d, x, ldx, W, y, ldy), (hipStream_t)stream); });
   return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
