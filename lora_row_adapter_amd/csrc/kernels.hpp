@@ -259,25 +259,35 @@ struct W4GemmArgs {
   int32_t tiles_m, tiles_n;
 };
 // The layer for at most kW4Rows rows, without a plan: launch_w4_shrink checks
-// the rows (row[], the counts in hdr) and writes t = scale_s x A_s^T of each
-// row's own adapter s, as two bf16 whose sum keeps 16 bits, and the product adds
-// t B_s^T to its sums.
+// the rows (row[], rank[], the counts in hdr) and writes t = scale_s x A_s^T of
+// each row's own adapter s, as two bf16 whose sum keeps 16 bits, and the product
+// adds t B_s^T to its own sums.
 constexpr int kW4Rows = 64;
 struct W4Lora {
   int32_t n_slices, S, M;
-  int32_t Rp;               // rows of t: max rank over slices rounded up to 32
+  int32_t Rp;                 // row of t: max rank over slices rounded up to 8
   SliceRef sl[kMaxSlices];
   int64_t n_pages[kMaxSlices];
   const int32_t *ids;
-  int32_t *hdr;             // counts of bad ids, ranks, pages (HdrWord)
-  int32_t *row;             // [M]: the adapter to apply, or -1
-  uint16_t *t_hi, *t_lo;    // [n_slices, M, Rp]
+  int32_t *hdr;               // counts of bad ids, ranks, pages (HdrWord)
+  int32_t *row;               // [M]: the adapter to apply, or -1
+  int32_t *rank;              // [n_slices, M]: its rank, or 0
+  uint16_t *t_hi, *t_lo;      // [n_slices, M, Rp], zeros past the rank
   const uint16_t *x;
   int64_t ldx, k;
 };
+// Reads every line of the arguments once: they lie in host memory, and read as
+// they are needed each would be waited for on its own.
+__device__ __forceinline__ void touch(const W4Lora &a) {
+  uint32_t v = (uint32_t)(uintptr_t)a.t_hi;
+#pragma unroll
+  for (int q = 0; q < kMaxSlices; ++q) v ^= (uint32_t)a.sl[q].col0 ^ (uint32_t)a.sl[q].ar.max_pages;
+  v ^= (uint32_t)a.n_pages[0] ^ (uint32_t)a.ldx;
+  asm volatile("" ::"s"(v));
+}
 hipError_t launch_w4_shrink(const W4Lora &a, hipStream_t st);
-// Bytes of row[] and t.
-size_t w4_lora_bytes(int64_t M, int32_t n_slices, int32_t R);
+// Sets, in `bytes` bytes at `at`, row, rank and t; false where they do not fit.
+bool w4_lora_place(W4Lora &a, uint8_t *at, size_t bytes);
 // plan: run it in this launch, in a workgroup beside the tiles (only where
 // gemm_w4_runs_plan says so); lora: add this (at most kW4Rows rows that
 // gemm_w4_adds_lora accepts).

@@ -542,23 +542,18 @@ static lora_status_t run_w4_rows(const LoraArgs &a, const W4GemmArgs &g, const W
   l.n_slices = a.n_slices;
   l.S = S;
   l.M = g.M;
-  l.Rp = (a.R + 31) & ~31;
+  l.Rp = (a.R + 7) & ~7;
   for (int q = 0; q < a.n_slices; ++q) {
     l.sl[q] = a.sl[q];
     l.n_pages[q] = slices[q].adapters.n_pages;
   }
   l.ids = ids;
   l.hdr = reinterpret_cast<int32_t *>(a.ws + L.hdr);
-  // in the place of the shrink's partials, which are 16 times as many
-  uint8_t *at = a.ws + L.tpart;
-  const size_t t = (size_t)a.n_slices * g.M * l.Rp * sizeof(uint16_t);
-  l.t_hi = reinterpret_cast<uint16_t *>(at);
-  l.t_lo = reinterpret_cast<uint16_t *>(at + t);
-  l.row = reinterpret_cast<int32_t *>(at + 2 * t);
-  if (L.tpart + w4_lora_bytes(g.M, a.n_slices, a.R) > L.total) return LORA_ERR_WORKSPACE;
   l.x = g.x;
   l.ldx = g.ldx;
   l.k = g.K;
+  // in the place of the plan's shrink partials
+  if (!w4_lora_place(l, a.ws + L.tpart, L.total - L.tpart)) return LORA_ERR_WORKSPACE;
   hipError_t e = timed(LORA_K_SGMV_SHRINK, st, [&] { return launch_w4_shrink(l, st); });
   if (e != hipSuccess) return LORA_ERR_HIP;
   e = timed(LORA_K_GEMM, st, [&] { return launch_gemm_w4(g, st, nullptr, &l); });

@@ -173,85 +173,199 @@ struct Nothing {};
 template <With kWith>
 using with_t = std::conditional_t<kWith == kPlan, PlanArgs, std::conditional_t<kWith == kLora, W4Lora, Nothing>>;
 
-// B_s[n][j .. j + 7] of slice q, zeros from the rank r on.
-__device__ __forceinline__ bf16x8_t load_b(const SliceRef &sl, int s, int r, int64_t n, int j) {
-  u32x4_t v = {0, 0, 0, 0};
-  if (j < r) {
-    const int stride = sl.ar.pooled ? r : sl.ar.max_rank;  // of B's rows
-    if (stride % 8 == 0) {  // whole vectors, of one page
-      v = *reinterpret_cast<const u32x4_t *>(adapter_b_ptr(sl.ar, s, r, n, j));
-      if (r - j < 8) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (2 * e >= r - j) v[e] = 0;
-          else if (2 * e + 1 >= r - j) v[e] &= 0xFFFFu;
-        }
-      }
-    } else {
-      for (int e = 0; e < 8 && j + e < r; ++e)
-        v[e >> 1] |= (uint32_t)*reinterpret_cast<const uint16_t *>(adapter_b_ptr(sl.ar, s, r, n, j + e)) << (16 * (e & 1));
-    }
-  }
-  return __builtin_bit_cast(bf16x8_t, v);
-}
+// The adapters' part of a workgroup's rows and columns, t B_s^T, is the work of
+// lora_waves more waves: what it waits for, one after the other (the rows'
+// adapters, then their B), passes while the others stream W.  8192 x 9216, one row: 9
+// us without it, 10 so, 13 - 14 where the same waves did it before, in or after their
+// own records; 16 rows of 12 adapters: 14 so, 16 - 19.
+template <int FM>
+constexpr int lora_waves = FM == 1 ? 8 : 4;  // as many as FM row tiles of W leave registers for
 
-// Adds t B_s^T to the sums of this workgroup's rows, each distinct adapter and
-// 16 columns the work of one of its waves.  A product is taken for all 16 rows of
-// a tile and added to those of that adapter alone, so no adapter's values reach
-// another's rows.
-template <int FM, int FN, int NW>
-__device__ __forceinline__ void add_lora(const W4Lora &l, int m0, int n0, int N, int wave,
-                                         f32x4_t (&tot)[FM][FN]) {
-  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
-  const int own = lane < 16 * FM && m0 + lane < l.M ? l.row[m0 + lane] : -1;  // of row m0 + lane
-  uint64_t left = __ballot(own >= 0);
-  for (int c = 0; left != 0; c += FN) {
-    const int s = __builtin_amdgcn_readlane(own, __builtin_ctzll(left));
-    const uint64_t mine = __ballot(own == s);
-    left &= ~mine;
+// Each distinct adapter and 16 columns are one unit, kAhead of them with their B on its
+// way at once.  A product is taken for all rows of a tile and added to those of that
+// adapter alone, so no adapter's values reach another's rows.
+template <int FM, int FN>
+struct LoraPart {
+  static constexpr int ROWS = 16 * FM, kAhead = 3;
+  const W4Lora &l;
+  const int m0, n0, lane, r, h;
+  const int M, Rp;
+  int own, lrank;            // of row m0 + lane
+  int q, k0;                 // the slice, the first of 64 ranks
+  int first, d;              // this lane's first column in the slice, its columns
+  uint64_t of[kAhead];       // units: rows, 16 columns, adapter, rank, B
+  int at[kAhead], us[kAhead], ur[kAhead];
+  u32x4_t b[kAhead][2];
+  u32x4_t t[2][FM][2];       // high and low parts
+
+  __device__ __forceinline__ LoraPart(const W4Lora &l, int m0, int n0)
+      : l(l), m0(m0), n0(n0), lane(threadIdx.x & 63), r(lane & 15), h(lane >> 4), M(l.M), Rp(l.Rp) {}
+
+  // A value of each row: 0: its adapter, 1 + q: its rank in slice q.
+  __device__ __forceinline__ int of_row(const int32_t *rows, int i) const {
+    return rows[i * M + m0 + min(lane, min(ROWS, M - m0) - 1)];
+  }
+  __device__ __forceinline__ void load_t() {
+    const uint32_t bytes = (uint32_t)(l.n_slices * M * Rp * 2);
+    const auto rh = rsrc(l.t_hi, bytes), rl = rsrc(l.t_lo, bytes);
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      if ((c + j) % NW != wave) continue;
-      const int n = n0 + 16 * j + r;
-      for (int q = 0; q < l.n_slices; ++q) {
-        const SliceRef &sl = l.sl[q];
-        const int64_t at = n - sl.col0;
-        if (n0 + 16 * j + 15 < sl.col0 || n0 + 16 * j >= sl.col0 + sl.d) continue;
-        const int rank = sl.ranks[s], full = (rank + 15) & ~15;  // t is written up to there
-        const bool in = n < N && at >= 0 && at < sl.d;
-        f32x4_t acc[FM];
+    for (int m = 0; m < FM; ++m)
 #pragma unroll
-        for (int m = 0; m < FM; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-        for (int k0 = 0; k0 < rank; k0 += 32) {
-          const int k = k0 + 8 * h;
-          const bf16x8_t b = load_b(sl, s, in ? rank : 0, in ? at : 0, k);
+      for (int c = 0; c < 2; ++c) {
+        const int row = m0 + 16 * m + r, j = k0 + 32 * c + 8 * h;
+        const uint32_t off = row < M && j < Rp ? (uint32_t)((q * M + row) * Rp + j) * 2 : kOob;
+        t[0][m][c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rh, off, 0, 0));
+        t[1][m][c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rl, off, 0, 0));
+      }
+  }
+  // Of this lane's column of unit i: ranks of B in the eight from k0 + 32 c + 8 h on.
+  __device__ __forceinline__ int ranks(int i, int c) const {
+    const int n = first + 16 * at[i];
+    return of[i] != 0 && n >= 0 && n < d ? max(0, min(8, ur[i] - (k0 + 32 * c + 8 * h))) : 0;
+  }
+  __device__ __forceinline__ void load_b() {
+    const AdapterRef &ar = l.sl[q].ar;
+    if (!ar.pooled) {
+      const uint8_t *B = ar.B;
+      const uint32_t R2 = ar.max_rank * 2, rows = (uint32_t)d * R2;
 #pragma unroll
-          for (int m = 0; m < FM; ++m) {
-            u32x4_t hi = {0, 0, 0, 0}, lo = hi;
-            if (k < full && (mine >> (16 * m + r) & 1)) {
-              const int64_t o = ((int64_t)q * l.M + m0 + 16 * m + r) * l.Rp + k;
-              hi = *reinterpret_cast<const u32x4_t *>(l.t_hi + o);
-              lo = *reinterpret_cast<const u32x4_t *>(l.t_lo + o);
-            }
-            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, hi), b, acc[m], 0, 0, 0);
-            acc[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, lo), b, acc[m], 0, 0, 0);
-          }
+      for (int i = 0; i < kAhead; ++i) {
+        if (i > 0 && of[i] == 0) break;
+        const auto rb = rsrc(B + (int64_t)us[i] * rows, rows);
+        const uint32_t off = (uint32_t)(first + 16 * at[i]) * R2 + (k0 + 8 * h) * 2;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          b[i][c] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rb, ranks(i, c) > 0 ? off + 64 * c : kOob, 0, 0));
+      }
+      return;
+    }
+    // lanes with no rank load the pool's first bytes; places in 16 bytes
+    const uint32_t k8 = (uint32_t)ar.k, shift = ar.page_shift - 4, mask = (uint32_t)(ar.page_bytes >> 4) - 1;
+    uint32_t off[kAhead][2];
+    int32_t page[kAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const uint32_t at16 = (uint32_t)ur[i] / 8 * (k8 + first + 16 * at[i]) + k0 / 8 + 4 * c + h;
+        off[i][c] = ranks(i, c) > 0 ? at16 : 0;
+        page[i][c] = ar.page_table[(int64_t)us[i] * ar.max_pages + (off[i][c] >> shift)];
+      }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int64_t pg = ranks(i, c) > 0 ? page[i][c] : 0;
+        b[i][c] = *reinterpret_cast<const u32x4_t *>(ar.pool + (pg << ar.page_shift) + (int64_t)(off[i][c] & mask) * 16);
+      }
+  }
+  // The same where B's rows are no whole 16-byte vectors.
+  __device__ __forceinline__ void load_b_by_rank() {
+    const AdapterRef &ar = l.sl[q].ar;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        b[i][c] = u32x4_t{0, 0, 0, 0};
+        const int n = ranks(i, c);
+#pragma unroll 1
+        for (int e = 0; e < n; ++e) {
+          const uint32_t one = *reinterpret_cast<const uint16_t *>(
+              adapter_b_ptr(ar, us[i], ur[i], first + 16 * at[i], k0 + 32 * c + 8 * h + e));
+#pragma unroll
+          for (int g = 0; g < 4; ++g) b[i][c][g] |= g == e >> 1 ? one << (16 * (e & 1)) : 0;
         }
+      }
+  }
+  __device__ __forceinline__ void products(f32x4_t (&tot)[FM][FN]) {
 #pragma unroll
-        for (int m = 0; m < FM; ++m)
+    for (int i = 0; i < kAhead; ++i) {
+      if (of[i] == 0) return;
+      if (ur[i] % 8 != 0 || l.sl[q].ar.pooled) {  // nothing past the rank
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (in && (mine >> (16 * m + 4 * h + e) & 1)) tot[m][j][e] += acc[m][e];
+        for (int c = 0; c < 2; ++c) {
+          const int n = ranks(i, c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[i][c][e] = 2 * e + 1 < n ? b[i][c][e] : 2 * e < n ? b[i][c][e] & 0xFFFFu : 0u;
+        }
+      }
+      const bool in = first + 16 * at[i] >= 0 && first + 16 * at[i] < d;
+      const uint64_t to = of[i] >> (4 * h);
+#pragma unroll
+      for (int m = 0; m < FM; ++m) {
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, t[p][m][c]),
+                                                          __builtin_bit_cast(bf16x8_t, b[i][c]), acc, 0, 0, 0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[e] = in && (to >> (16 * m + e) & 1) ? acc[e] : 0.f;
+#pragma unroll
+        for (int jj = 0; jj < FN; ++jj)
+          if (jj == at[i]) tot[m][jj] += acc;
       }
     }
   }
-}
+  // wave of lora_waves: every lora_waves-th unit, adapters in the order of their first
+  // rows, columns inside.
+  __device__ __forceinline__ void run(int wave, f32x4_t (&tot)[FM][FN]) {
+    const int32_t *rows = l.row;
+    own = of_row(rows, 0);
+    const bool live = lane < ROWS && m0 + lane < M;
+#pragma unroll 1
+    for (q = 0; q < l.n_slices; ++q) {
+      const SliceRef &sl = l.sl[q];
+      d = (int)sl.d;
+      first = n0 + r - (int)sl.col0;
+      if (first - r >= d || first - r + 16 * FN <= 0) continue;
+      lrank = of_row(rows, 1 + q);
+#pragma unroll 1
+      for (k0 = 0; k0 < sl.ar.max_rank; k0 += 64) {
+        load_t();
+        const bool has = live && own >= 0;
+        uint64_t left = __ballot(has && lrank > k0), mine = 0;  // rows of adapters to come
+        if (left == 0) break;
+        // B's rows of whole 16-byte vectors, each of one page
+        const bool vec = sl.ar.pooled ? __ballot(has && lrank % 8 != 0) == 0 : sl.ar.max_rank % 8 == 0;
+        int s = 0, rk = 0, j = FN + wave;  // the unit's columns, FN more for each adapter to pass
+#pragma unroll 1
+        while (true) {
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            while (j >= FN && left != 0) {
+              const int f = __builtin_ctzll(left);
+              s = __builtin_amdgcn_readlane(own, f);
+              rk = __builtin_amdgcn_readlane(lrank, f);
+              mine = __ballot(own == s) & left;
+              left &= ~mine;
+              j -= FN;
+            }
+            of[i] = j < FN ? mine : 0;
+            at[i] = j < FN ? j : 0;
+            us[i] = s;
+            ur[i] = rk;
+            j += lora_waves<FM>;
+          }
+          if (of[0] == 0) break;
+          if (vec) load_b();
+          else load_b_by_rank();
+          products(tot);
+          if (of[kAhead - 1] == 0) break;
+        }
+      }
+    }
+  }
+};
 
 template <int FM, int FN, int NW, int PD, int SG, With kWith>
-__global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p, with_t<kWith> with) {
+__global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM> : 0))) void k_w4_split(W4GemmArgs p,
+                                                                                              with_t<kWith> with) {
   constexpr int REC = (int)w4_record(SG), KS = 4 / SG;
   constexpr int HALF = FM * 2048, XI = 2 * FM;  // x: bytes of half a record, loads of 1 KiB
-  constexpr int RING = NW * PD * 2 * HALF, PART = NW * FM * FN * 1024;
+  constexpr int ALL = NW + (kWith == kLora ? lora_waves<FM> : 0);
+  constexpr int RING = NW * PD * 2 * HALF, PART = ALL * FM * FN * 1024;
   constexpr int kYounger = XI + (PD - 1) * (FN * (1 + SG) + 2 * XI) + FN * (1 + SG);
   constexpr int PLAN = kWith == kPlan ? (int)plan_detail::plan_sort_lds(plan_detail::kPlanRowBitsMax) : 0;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[std::max({RING, PART, PLAN})];
@@ -304,64 +418,67 @@ __global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p, with_t<kWith
     for (int j = 0; j < FN; ++j) tot[m][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
   const f32x4_t zero = {0.f, 0.f, 0.f, 0.f};
   const uint32_t xa = lds_addr(ring) + r * 128;
+  if (kWith == kLora && wave >= NW) {
+    if constexpr (kWith == kLora) {
+      touch(with);
+      LoraPart<FM, FN>(with, m0, n0).run(wave - NW, tot);
+    }
+  } else {
 #pragma unroll
-  for (int d = 0; d < PD; ++d) {
-    load_w(d, d);
-    asm volatile("" ::: "memory");
-    load_x(d, d, 0);
-    load_x(d, d, 1);
-    asm volatile("" ::: "memory");
-  }
-  if constexpr (kWith == kLora) {  // while the first records are on their way
-    add_lora<FM, FN, NW>(with, m0, n0, p.N, wave, tot);
-    asm volatile("" ::: "memory");
-  }
-  for (int t0 = 0; t0 < cnt; t0 += PD) {
+    for (int d = 0; d < PD; ++d) {
+      load_w(d, d);
+      asm volatile("" ::: "memory");
+      load_x(d, d, 0);
+      load_x(d, d, 1);
+      asm volatile("" ::: "memory");
+    }
+    for (int t0 = 0; t0 < cnt; t0 += PD) {
 #pragma unroll
-    for (int d = 0; d < PD; ++d) {  // past the last record: zeros by zeros
-      u32x4_t wc[FN];
-      float s[FN][SG], z[FN][SG];
+      for (int d = 0; d < PD; ++d) {  // past the last record: zeros by zeros
+        u32x4_t wc[FN];
+        float s[FN][SG], z[FN][SG];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        wc[j] = wq[d][j];
+        for (int j = 0; j < FN; ++j) {
+          wc[j] = wq[d][j];
 #pragma unroll
-        for (int g = 0; g < SG; ++g) {
-          s[j][g] = scale_of(sq[d][j][g]);
-          z[j][g] = (float)(sq[d][j][g] & 31u);
+          for (int g = 0; g < SG; ++g) {
+            s[j][g] = scale_of(sq[d][j][g]);
+            z[j][g] = (float)(sq[d][j][g] & 31u);
+          }
         }
-      }
-      load_w(t0 + d + PD, d);
-      f32x4_t acc[FM][FN], sum[FM];
+        load_w(t0 + d + PD, d);
+        f32x4_t acc[FM][FN], sum[FM];
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        // Loads younger than this half's: the other half's of the same record or
-        // the one before, W's and x's of the records between, W's just above.
-        asm volatile("" ::: "memory");
-        wait_vm<std::min(kYounger, 63)>();
-        u32x4_t xf[2][FM];
-        const uint32_t at = xa + (d * 2 + u) * HALF;
-        read_half<FM>(at + (h ^ (r & 7)) * 16, at + ((4 + h) ^ (r & 7)) * 16, xf);
-        load_x(t0 + d + PD, d, u);
-        asm volatile("" ::: "memory");
+        for (int u = 0; u < 2; ++u) {
+          // Loads younger than this half's: the other half's of the same record or
+          // the one before, W's and x's of the records between, W's just above.
+          asm volatile("" ::: "memory");
+          wait_vm<std::min(kYounger, 63)>();
+          u32x4_t xf[2][FM];
+          const uint32_t at = xa + (d * 2 + u) * HALF;
+          read_half<FM>(at + (h ^ (r & 7)) * 16, at + ((4 + h) ^ (r & 7)) * 16, xf);
+          load_x(t0 + d + PD, d, u);
+          asm volatile("" ::: "memory");
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int ks = 2 * u + i, g = ks / KS;
-          const bool first = ks % KS == 0, last = ks % KS == KS - 1;
+          for (int i = 0; i < 2; ++i) {
+            const int ks = 2 * u + i, g = ks / KS;
+            const bool first = ks % KS == 0, last = ks % KS == KS - 1;
 #pragma unroll
-          for (int m = 0; m < FM; ++m)
-            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), ones8(),
-                                                             first ? zero : sum[m], 0, 0, 0);
+            for (int m = 0; m < FM; ++m)
+              sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), ones8(),
+                                                               first ? zero : sum[m], 0, 0, 0);
 #pragma unroll
-          for (int j = 0; j < FN; ++j) {
-            const bf16x8_t wf = codes(wc[j][ks]);
+            for (int j = 0; j < FN; ++j) {
+              const bf16x8_t wf = codes(wc[j][ks]);
 #pragma unroll
-            for (int m = 0; m < FM; ++m) {
-              acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), wf,
-                                                                  first ? zero : acc[m][j], 0, 0, 0);
-              if (last) {
+              for (int m = 0; m < FM; ++m) {
+                acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xf[i][m]), wf,
+                                                                    first ? zero : acc[m][j], 0, 0, 0);
+                if (last) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  tot[m][j][e] = __builtin_fmaf(s[j][g], __builtin_fmaf(-z[j][g], sum[m][e], acc[m][j][e]), tot[m][j][e]);
+                  for (int e = 0; e < 4; ++e)
+                    tot[m][j][e] = __builtin_fmaf(s[j][g], __builtin_fmaf(-z[j][g], sum[m][e], acc[m][j][e]), tot[m][j][e]);
+                }
               }
             }
           }
@@ -377,10 +494,10 @@ __global__ __launch_bounds__(64 * NW) void k_w4_split(W4GemmArgs p, with_t<kWith
 #pragma unroll
     for (int j = 0; j < FN; ++j) part[wave][m * FN + j][lane] = tot[m][j];
   __syncthreads();
-  for (int u = wave; u < FM * FN; u += NW) {
+  for (int u = wave; u < FM * FN; u += ALL) {
     f32x4_t v = part[0][u][lane];
 #pragma unroll
-    for (int q = 1; q < NW; ++q) v += part[q][u][lane];
+    for (int q = 1; q < ALL; ++q) v += part[q][u][lane];
     const int n = n0 + u % FN * 16 + r, m = m0 + u / FN * 16 + 4 * h;
     if (n >= p.N) continue;
 #pragma unroll
@@ -395,12 +512,19 @@ struct Extra {
   const W4Lora *lora;
 };
 
+constexpr int kLoraTiles = 2;  // of rows at most where the adapters' part is added: registers for twelve waves
+
 template <int FM, int FN, int NW, int PD, int SG>
 void launch_split(const W4GemmArgs &a, const Extra &x, hipStream_t st) {
   const dim3 grid((a.N + 16 * FN - 1) / (16 * FN) + (x.plan ? 1 : 0), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
-  if (x.plan) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kPlan>), grid, block, 0, st, a, *x.plan);
-  else if (x.lora) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kLora>), grid, block, 0, st, a, *x.lora);
-  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kNone>), grid, block, 0, st, a, Nothing{});
+  if (x.plan) {
+    hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kPlan>), grid, block, 0, st, a, *x.plan);
+  } else if (x.lora) {
+    if constexpr (FM <= kLoraTiles)
+      hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kLora>), grid, dim3(64 * (NW + lora_waves<FM>)), 0, st, a, *x.lora);
+  } else {
+    hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kNone>), grid, block, 0, st, a, Nothing{});
+  }
 }
 template <int FM, int FN, int NW, int PD>
 void launch_split(W4GemmArgs a, const Extra &x, hipStream_t st) {
@@ -755,7 +879,7 @@ struct Cost {
 struct Shape {
   int bm, bn;
   bool rounds;  // the weights, to bf16
-  int held;      // workgroups that a CU holds
+  int held;     // workgroups that a CU holds
   Cost cost[3];  // groups of 128 and more, 64, 32
   void (*launch)(W4GemmArgs, const Extra &, hipStream_t);
 };
@@ -777,9 +901,9 @@ const Shape kShapes[] = {
     split<1, 3, 8, 1>({2, 2.35f, 1.15f, 0.f, 0.0636f, 0.047f},
                      {2, 2.f, 1.48f, 0.0035f, 0.0922f, 0.0322f},
                      {2, 2.08f, 1.2f, 0.031f, 0.114f, 0.0278f}),
-    split<1, 2, 16, 1>({1, 2.32f, 1.16f, 0.0401f, 0.f, 0.0389f},
-                     {1, 2.17f, 1.25f, 0.0534f, 0.f, 0.034f},
-                     {1, 2.14f, 1.27f, 0.0779f, 0.f, 0.0333f}),
+    split<1, 2, 8, 1>({4, 1.49f, 1.96f, 0.f, 0.0411f, 0.0302f},
+                     {2, 2.54f, 0.854f, 0.f, 0.0535f, 0.0244f},
+                     {2, 2.08f, 1.27f, 0.0147f, 0.074f, 0.0207f}),
     split<2, 2, 8, 1>({1, 2.7f, 0.671f, 0.0782f, 0.f, 0.0368f},
                      {1, 2.6f, 0.75f, 0.0883f, 0.f, 0.0372f},
                      {1, 2.74f, 0.711f, 0.136f, 0.f, 0.0148f}),
@@ -803,11 +927,13 @@ const Shape kShapes[] = {
     tile<8, 4, 2, 4, 1, 3, 2>({1, 0.f, 6.5f, 2.68f, 0.f, 0.733f}),
 };
 
-const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
+// lora: with the adapters' part.  The shapes that add it give every row the same
+// sums as those that the product takes for as many rows.
+const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg, bool lora = false) {
   const Shape *best = nullptr;
   double least = 0;
   for (const Shape &h : kShapes) {
-    if (h.rounds && M <= kW4Rows) continue;  // the adapters' part goes with the others
+    if ((h.rounds && M <= kW4Rows) || (lora && h.bm > 16 * kLoraTiles)) continue;
     const Cost &c = h.cost[sg >> 1];
     const int64_t tiles = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
     const double rounds = (double)((tiles + 256 * c.fit - 1) / (256 * c.fit)), cu = (double)((tiles + 255) / 256);
@@ -873,7 +999,7 @@ hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs 
       a.w += n0 / 16 * a.nb * w4_record(a.sg);
       a.y += m0 * a.ldy + n0;
       if (!far) {
-        best_of(a.M, a.N, a.nb, a.sg).launch(a, Extra{plan, lora}, st);
+        best_of(a.M, a.N, a.nb, a.sg, lora != nullptr).launch(a, Extra{plan, lora}, st);
       } else {
         const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
         if (a.sg == 1) hipLaunchKernelGGL(k_w4_far<1>, grid, dim3(256), 0, st, a);

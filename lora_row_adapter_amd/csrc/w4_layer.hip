@@ -1,20 +1,29 @@
 // w4_layer.hip -- the 4-bit layer for at most 64 rows (include/lora_w4.h): what
 // goes ahead of the product that adds the adapters' part itself (w4.hip).
 //
-// With so few rows a plan has little to sort and its launch, and the fork and
+// With so few rows a plan has little to sort, and its launch, and the fork and
 // join beside the product, cost more than the rest of the layer.  Here each
-// workgroup finds by itself whether it has work: workgroup (row u, slice,
-// sixteen ranks) serves all rows of row u's adapter unless an earlier row has the
-// same one, and takes its sixteen rows of A over all of k (sixteen waves, every
-// second kilobyte of it on its way at once).  Workgroup 0 checks the rows, as the plan
-// does, and writes which adapter each is to get.
+// workgroup finds by itself which rows it serves: up to four with one adapter, and of
+// their t one slice's next few ranks.  Workgroup 0 checks the rows, as the plan does,
+// and writes which adapter each is to get.
+//
+// What bounds it are the bytes of A at many adapters, and at few what a CU takes
+// in: 64 bytes a clock where a wave's load is one run of memory, as here (each lane
+// eight columns of one row of A), a quarter of that where it is 16 rows of 64 bytes,
+// as matrix instructions would have it.  At two slices of 64 ranks x 8192: one row
+// 4.5 us (2.2 of them the launch and the rows' checks; 10.5 with matrix instructions and
+// all of k to a workgroup), 16 rows of 12 adapters 7.5 (25 MB of A).
+#include <algorithm>
+
 #include "kernels.hpp"
 
 namespace lora {
 
 namespace {
 
-constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kThreads = 512, kWaves = kThreads / 64;
+constexpr int kRows = 4;    // of an adapter at a time
+constexpr int kFill = 512;  // workgroups aimed at
 
 // Pages that adapter s needs in slice q (0 in slots), or -1: past its table.
 __device__ __forceinline__ int64_t pages_of(const W4Lora &a, int q, int r) {
@@ -72,7 +81,10 @@ __device__ __forceinline__ void check_rows(const W4Lora &a, int id) {
   __syncthreads();
   if (wave != 0) return;
   const bool paged = ranked && bad[lead] == 0;
-  if (lane < a.M) a.row[lane] = paged ? id : -1;
+  if (lane < a.M) {
+    a.row[lane] = paged ? id : -1;
+    for (int q = 0; q < a.n_slices; ++q) a.rank[q * a.M + lane] = paged ? a.sl[q].ranks[id] : 0;
+  }
   const bool live = lane < a.M;
   const uint64_t ids = __ballot(live && id != -1 && !known), ranks = __ballot(live && known && !ranked),
                  pages = __ballot(live && ranked && !paged);
@@ -83,91 +95,153 @@ __device__ __forceinline__ void check_rows(const W4Lora &a, int id) {
   }
 }
 
+// A_s[j][k .. k + 7]; zeros where its page is none of the pool's, as such a row's
+// t is not used.
+__device__ __forceinline__ u32x4_t load_a(const AdapterRef &ar, int64_t n_pages, int s, int j, int64_t k) {
+  const int64_t off = ((int64_t)j * ar.k + k) * 2;
+  const uint8_t *at = ar.A + (int64_t)s * ar.max_rank * ar.k * 2 + off;
+  if (ar.pooled) {
+    const int32_t pg = ar.page_table[(int64_t)s * ar.max_pages + (off >> ar.page_shift)];
+    if (pg < 0 || pg >= n_pages) return u32x4_t{0, 0, 0, 0};
+    at = ar.pool + ((int64_t)pg << ar.page_shift) + (off & (ar.page_bytes - 1));
+  }
+  return *reinterpret_cast<const u32x4_t *>(at);
+}
+
+template <int kCtrl>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), kCtrl, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), lane));
+}
+// The sum over a wave's lanes.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = add_dpp<0xB1>(v);   // lanes 1 0 3 2
+  v = add_dpp<0x4E>(v);   // lanes 2 3 0 1
+  v = add_dpp<0x141>(v);  // lanes 7 .. 0
+  v = add_dpp<0x140>(v);  // lanes 15 .. 0
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+__device__ __forceinline__ float bf16_at(u32x4_t v, int i) {
+  return __builtin_bit_cast(float, i & 1 ? v[i >> 1] & 0xFFFF0000u : v[i >> 1] << 16);
+}
+
+// kRanks: of a workgroup.
+template <int kRanks>
 __global__ __launch_bounds__(kThreads) void k_w4_shrink(W4Lora a, int jblocks) {
-  __shared__ f32x4_t part[kWaves][64];
-  __shared__ int rows[kW4Rows];
-  const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
+  __shared__ float part[kWaves][kRows * kRanks];
+  const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  touch(a);
   const int id = lane < a.M ? a.ids[lane] : -1;
   if (blockIdx.x == 0) {
     check_rows(a, id);
     return;
   }
-  const int b = blockIdx.x - 1, u = b / (a.n_slices * jblocks), q = b / jblocks % a.n_slices, j0 = b % jblocks * 16;
-  const int s = __builtin_amdgcn_readlane(id, u);
-  if (s < 0 || s >= a.S) return;
-  const uint64_t mine = __ballot(id == s);
-  if (__builtin_ctzll(mine) != u) return;
+  // the v-th group of kRows rows with one adapter: its first row, slice, ranks
+  int b = blockIdx.x - 1;
+  const int j0 = b % jblocks * kRanks;
+  b /= jblocks;
+  const int q = b % a.n_slices, v = b / a.n_slices;
+  int same = 0;  // rows above this lane's with its adapter
+  for (int i = 0; i + 1 < a.M; ++i) same += i < lane && __builtin_amdgcn_readlane(id, i) == id;
+  const bool leads = id >= 0 && id < a.S && same % kRows == 0;
+  const uint64_t all = __ballot(leads);
+  const uint64_t found = __ballot(leads && (int)__popcll(all & ((uint64_t(1) << lane) - 1)) == v);
+  if (found == 0) return;
+  const int u = __builtin_ctzll(found);
+  const int s = __builtin_amdgcn_readlane(id, u), from = __builtin_amdgcn_readlane(same, u);
+  uint64_t mine = __ballot(id == s && same >= from && same < from + kRows);
   const SliceRef &sl = a.sl[q];
   const int rank = sl.ranks[s];
-  if (j0 >= rank || !ranks_ok(a, s)) return;
-  bool bad = false;
-  for (int p = 0; p < a.n_slices; ++p) {
-    const int64_t n = pages_of(a, p, a.sl[p].ranks[s]);
-    bad |= n < 0;
-    for (int64_t j = threadIdx.x; j < n; j += kThreads) bad |= bad_page(a, p, s, j);
-  }
-  const int cnt = (int)__popcll(mine);
-  if (wave == 0 && (mine >> lane & 1)) rows[__popcll(mine & ((uint64_t(1) << lane) - 1))] = lane;
-  if (__syncthreads_or(bad)) return;
-
   const float scale = sl.scales[s];
-  for (int t0 = 0; t0 < cnt; t0 += 16) {
-    const uint16_t *x = a.x + (int64_t)rows[min(t0 + r, cnt - 1)] * a.ldx;  // past the last: that, not kept
-    const int j = min(j0 + r, rank - 1);                                      // likewise
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kSteps = 8;
-    for (int64_t c = wave * (32 * kSteps); c < a.k; c += kWaves * 32 * kSteps) {
-      u32x4_t xv[kSteps], av[kSteps];
+  if (rank < 0 || rank > sl.ar.max_rank || pages_of(a, q, rank) < 0) return;
+  const int n = (int)__popcll(mine);
+  int row[kRows];
+  const uint16_t *x[kRows];
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int64_t k = c + 32 * i + 8 * h;
-        xv[i] = av[i] = u32x4_t{0, 0, 0, 0};
-        if (k < a.k) {
-          xv[i] = *reinterpret_cast<const u32x4_t *>(x + k);
-          av[i] = *reinterpret_cast<const u32x4_t *>(adapter_a_ptr(sl.ar, s, rank, j, k));
-        }
-      }
+  for (int i = 0; i < kRows; ++i) {
+    row[i] = mine != 0 ? __builtin_ctzll(mine) : row[i - 1];
+    mine &= mine - 1;
+    x[i] = a.x + (int64_t)row[i] * a.ldx;
+  }
+  float acc[kRows][kRanks] = {};
+  if (j0 < rank) {
+#pragma unroll 2
+    for (int64_t k = threadIdx.x * 8; k < a.k; k += kThreads * 8) {
+      u32x4_t av[kRanks], xv[kRows];
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
-        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, xv[i]),
-                                                      __builtin_bit_cast(bf16x8_t, av[i]), acc, 0, 0, 0);
+      for (int e = 0; e < kRanks; ++e)  // past the rank: the last again, not kept
+        av[e] = load_a(sl.ar, a.n_pages[q], s, min(j0 + e, rank - 1), k);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (i < n) xv[i] = *reinterpret_cast<const u32x4_t *>(x[i] + k);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i)
+        if (i < n)
+#pragma unroll
+          for (int e = 0; e < kRanks; ++e)
+#pragma unroll
+            for (int c = 0; c < 8; ++c) acc[i][e] = __builtin_fmaf(bf16_at(xv[i], c), bf16_at(av[e], c), acc[i][e]);
     }
-    part[wave][lane] = acc;
-    __syncthreads();
-    if (wave == 0) {
-      f32x4_t v = part[0][lane];
+  }
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) v += part[w][lane];
+  for (int i = 0; i < kRows; ++i)
+    if (i < n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (t0 + 4 * h + e >= cnt) continue;
-        // zeros from the rank to the sixteen's end, where the product reads on
-        const float t = j0 + r < rank ? v[e] * scale : 0.f;
-        const uint16_t hi = f32_to_bf16_bits(t);
-        const float rest = t - bf16_bits_to_f32(hi);
-        const int64_t o = ((int64_t)q * a.M + rows[t0 + 4 * h + e]) * a.Rp + j0 + r;
-        a.t_hi[o] = hi;
-        // of an infinity or a NaN: nothing
-        a.t_lo[o] = rest - rest == 0.f ? f32_to_bf16_bits(rest) : 0;
+      for (int e = 0; e < kRanks; ++e) {
+        const float v = wave_sum(acc[i][e]);
+        if (lane == 0) part[wave][i * kRanks + e] = v;
       }
+  __syncthreads();
+  if ((int)threadIdx.x < n * kRanks) {
+    const int j = j0 + threadIdx.x % kRanks;
+    float v = part[0][threadIdx.x];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += part[w][threadIdx.x];
+    const float t = j < rank ? v * scale : 0.f;
+    const uint16_t hi = f32_to_bf16_bits(t);
+    const float rest = t - bf16_bits_to_f32(hi);
+    int to = row[0];
+#pragma unroll
+    for (int i = 1; i < kRows; ++i) to = (int)threadIdx.x / kRanks == i ? row[i] : to;
+    const int64_t o = ((int64_t)q * a.M + to) * a.Rp + j;
+    if (j < a.Rp) {
+      a.t_hi[o] = hi;
+      a.t_lo[o] = rest - rest == 0.f ? f32_to_bf16_bits(rest) : 0;  // of an infinity or a NaN: nothing
     }
-    __syncthreads();
   }
 }
 
 }  // namespace
 
-size_t w4_lora_bytes(int64_t M, int32_t n_slices, int32_t R) {
-  const int64_t Rp = (R + 31) & ~31;
-  return (size_t)(n_slices * M * Rp * 4 + M * 4);
+bool w4_lora_place(W4Lora &a, uint8_t *at, size_t bytes) {
+  const size_t t = (size_t)a.n_slices * a.M * a.Rp * sizeof(uint16_t), rows = (size_t)a.M * sizeof(int32_t);
+  a.t_hi = reinterpret_cast<uint16_t *>(at);
+  a.t_lo = reinterpret_cast<uint16_t *>(at + t);
+  a.row = reinterpret_cast<int32_t *>(at + 2 * t);
+  a.rank = a.row + a.M;
+  return 2 * t + rows * (1 + a.n_slices) <= bytes;
+}
+
+// At most, of kRows rows with one adapter.
+static int groups_of(const W4Lora &a) { return std::min(a.M, std::min(a.M, a.S) + a.M / kRows); }
+
+template <int kRanks>
+static void launch_shrink(const W4Lora &a, hipStream_t st) {
+  const int jblocks = (a.Rp + kRanks - 1) / kRanks;
+  hipLaunchKernelGGL(k_w4_shrink<kRanks>, dim3((unsigned)(1 + groups_of(a) * a.n_slices * jblocks)), dim3(kThreads), 0, st, a,
+                     jblocks);
 }
 
 hipError_t launch_w4_shrink(const W4Lora &a, hipStream_t st) {
-  int32_t R = 0;
-  for (int q = 0; q < a.n_slices; ++q) R = R > a.sl[q].ar.max_rank ? R : a.sl[q].ar.max_rank;
-  const int jblocks = (R + 15) / 16;
-  hipLaunchKernelGGL(k_w4_shrink, dim3((unsigned)(1 + a.M * a.n_slices * jblocks)), dim3(kThreads), 0, st, a, jblocks);
+  // as many ranks to a workgroup, up to four, as leave two workgroups for each CU where
+  // the groups are as many as they can be
+  const int64_t ranks = (int64_t)groups_of(a) * a.n_slices * a.Rp;
+  if (ranks < 2 * kFill) launch_shrink<1>(a, st);
+  else if (ranks < 4 * kFill) launch_shrink<2>(a, st);
+  else launch_shrink<4>(a, st);
   return hipGetLastError();
 }
 

@@ -348,6 +348,65 @@ def test_layer(case, pools):
         assert chk["n_bad_ids"] == chk["n_bad_ranks"] == chk["n_bad_pages"] == chk["n_sync_expired"] == 0
 
 
+FEW = [  # M, k, ds, group, max_rank, ranks: at and around 64 rows
+    (64, 520, (5, 7, 3, 40), 32, 256, [200]),             # one adapter's rows; slices inside 16 columns
+    (64, 264, (48, 17), 64, 64, list(range(1, 65))),      # an adapter for every row
+    (33, 1288, (33,), 128, 12, [12, 7, 1]),               # B's rows no whole vectors
+    (48, 4104, (16, 300), 128, 96, [96, 8, 64, 72, 0]),   # more than 64 ranks, k past what a workgroup takes
+    (65, 264, (48, 17), 64, 64, list(range(1, 65))),
+]
+
+
+@pytest.mark.parametrize("pools", [False, True])
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "%dx%s" % (c[0], "+".join(map(str, c[2]))))
+def test_layer_of_few_rows(case, pools):
+    M, k, ds, group, R_, ranks = case
+    say("w4 layer of few rows %s pools=%d" % (case, pools))
+    S = len(ranks)
+    rng = np.random.default_rng(M + S)
+    scales = rng.uniform(0.25, 4, S).astype(np.float32)
+    q, s, z = R.weight(M, sum(ds), k, group)
+    W = device_weight(q, s, z, group)
+    sets = [adapter_set(17 + i, S, R_, k, d, ranks, pad=float("nan")) for i, d in enumerate(ds)]
+    x = loud(M, M, k)
+    slices = device_slices(sets, ranks, scales, ds, k, R_, pools)
+    base = lr.lora_gemm_w4(x.cuda(), W)
+    for ids in (np.arange(M) % S, np.sort(rng.integers(0, S, M)), np.where(np.arange(M) == M // 2, S - 1, -1)):
+        ids = ids.astype(np.int32)
+        y = lr.lora_linear_sliced_w4(x.cuda(), W, slices, torch.from_numpy(ids).cuda())
+        want = layer_ref(x, R.dequant(q, s, z, group), ds, sets, ranks, scales.astype(np.float64), ids)
+        err = normwise(y.double().cpu().numpy(), want)
+        say("  normwise %.3g" % err)
+        assert err <= 2e-2
+        none = np.flatnonzero(ids < 0)
+        assert torch.equal(y[none], base[none])
+
+
+@pytest.mark.parametrize("M", [20, 64])
+def test_layer_keeps_an_adapters_nan_to_its_rows(M):
+    k, ds, ranks = 264, (40, 9), [8, 16, 5]
+    q, s, z = R.weight(2, sum(ds), k, 64)
+    W = device_weight(q, s, z, 64)
+    sets = [adapter_set(5 + i, 3, 16, k, d, ranks) for i, d in enumerate(ds)]
+    ids = torch.arange(M, dtype=torch.int32).cuda() % 3
+    x = loud(2, M, k).cuda()
+    run = lambda: lr.lora_linear_sliced_w4(x, W, device_slices(sets, ranks, [1.0] * 3, ds, k, 16), ids)
+    clean = run()
+    for A, B in sets:
+        A[1] = float("nan")
+        B[1, ::2] = float("inf")
+    y = run()
+    other = ids.cpu() != 1
+    assert torch.equal(y[other], clean[other])
+    assert y[~other].isnan().all()
+    for A, B in sets:  # an infinite t times finite B
+        A[1] = 3e38
+        B[1] = 1.0
+    y = run()
+    assert torch.equal(y[other], clean[other])
+    assert not torch.isfinite(y[~other].float()).any()
+
+
 @pytest.mark.parametrize("pools", [False, True])
 @pytest.mark.parametrize("M", [1, 3, 16, 33, 200])
 def test_layer_of_whole_numbers_exactly(M, pools):
