@@ -262,7 +262,7 @@ struct W4GemmArgs {
 // the rows (row[], rank[], the counts in hdr) and writes t = scale_s x A_s^T of
 // each row's own adapter s, as two bf16 whose sum keeps 16 bits, and the product
 // adds t B_s^T to its own sums.
-constexpr int kW4Rows = 64;
+constexpr int kW4Rows = 32;
 struct W4Lora {
   int32_t n_slices, S, M;
   int32_t Rp;                 // row of t: max rank over slices rounded up to 8
@@ -289,12 +289,13 @@ hipError_t launch_w4_shrink(const W4Lora &a, hipStream_t st);
 // Sets, in `bytes` bytes at `at`, row, rank and t; false where they do not fit.
 bool w4_lora_place(W4Lora &a, uint8_t *at, size_t bytes);
 // plan: run it in this launch, in a workgroup beside the tiles (only where
-// gemm_w4_runs_plan says so); lora: add this (at most kW4Rows rows that
-// gemm_w4_adds_lora accepts).
-hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st, const PlanArgs *plan = nullptr,
-                          const W4Lora *lora = nullptr);
+// gemm_w4_runs_plan says so).
+hipError_t launch_gemm_w4(const W4GemmArgs &a, hipStream_t st, const PlanArgs *plan = nullptr);
 bool gemm_w4_runs_plan(const W4GemmArgs &a);
+// The same with the adapters' part, only where gemm_w4_adds_lora says so.
+hipError_t launch_gemm_w4_lora(const W4GemmArgs &a, const W4Lora &l, hipStream_t st, const PlanArgs *plan);
 bool gemm_w4_adds_lora(const W4GemmArgs &a);
+bool gemm_w4_lora_runs_plan(const W4GemmArgs &a);
 // Index of the tile shape it takes; out: its rows, columns and whether it rounds
 // the weights to bf16.
 int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]);

@@ -534,10 +534,11 @@ static hipError_t run_mx_base(const MxBase &mx, int64_t Mc, int64_t k, int64_t d
   return launch_gemm_mx(g, st);
 }
 
-// The 4-bit layer for a few rows: two launches and no plan (the workspace's
-// plan regions stay as they are).
+// The 4-bit layer for a few rows: two launches that need no plan.  plan: make one all
+// the same, for calls that reuse it: in the product's launch, or where that has no room
+// for it ahead of it.
 static lora_status_t run_w4_rows(const LoraArgs &a, const W4GemmArgs &g, const WsLayout &L, int32_t S,
-                                 const lora_slice_t *slices, const int32_t *ids, hipStream_t st) {
+                                 const lora_slice_t *slices, const int32_t *ids, bool plan, hipStream_t st) {
   W4Lora l{};
   l.n_slices = a.n_slices;
   l.S = S;
@@ -554,9 +555,17 @@ static lora_status_t run_w4_rows(const LoraArgs &a, const W4GemmArgs &g, const W
   l.k = g.K;
   // in the place of the plan's shrink partials
   if (!w4_lora_place(l, a.ws + L.tpart, L.total - L.tpart)) return LORA_ERR_WORKSPACE;
+  PlanArgs pa{};
+  const bool beside = plan && gemm_w4_lora_runs_plan(g);
+  if (beside) {
+    pa = make_plan_args(g.M, g.K, LORA_DTYPE_BF16, a.n_slices, slices, ids, a.ws, L);
+  } else if (plan) {
+    const lora_status_t s = run_plan(g.M, g.K, LORA_DTYPE_BF16, a.n_slices, slices, ids, a.ws, L, st, kPlanLdsAlone);
+    if (s != LORA_OK) return s;
+  }
   hipError_t e = timed(LORA_K_SGMV_SHRINK, st, [&] { return launch_w4_shrink(l, st); });
   if (e != hipSuccess) return LORA_ERR_HIP;
-  e = timed(LORA_K_GEMM, st, [&] { return launch_gemm_w4(g, st, nullptr, &l); });
+  e = timed(LORA_K_GEMM, st, [&] { return launch_gemm_w4_lora(g, l, st, beside ? &pa : nullptr); });
   return e == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -633,7 +642,9 @@ lora_status_t linear_sliced_impl(lora_dtype_t dtype, int64_t M, int64_t k, const
 
   if (w4 && M <= kW4Rows && path != LORA_PATH_GATHER) {
     const W4GemmArgs g = make_w4_args(M, k, d_total, x, ldx, w4->W, y, ldy);
-    if (gemm_w4_adds_lora(g)) return run_w4_rows(a, g, ws_layout(M, S, R, n_slices), S, slices, adapter_ids, st);
+    if (gemm_w4_adds_lora(g))
+      return run_w4_rows(a, g, ws_layout(M, S, R, n_slices), S, slices, adapter_ids,
+                         !(flags & LORA_FLAG_REUSE_PLAN), st);
   }
 
   for (int64_t c0 = 0; c0 < M; c0 += kPlanMaxRows) {

@@ -167,19 +167,25 @@ __device__ __forceinline__ void read_half(uint32_t a0, uint32_t a1, u32x4_t (&x)
 // Loads past the end of a wave's records, of x's rows and of its columns are
 // past their buffer: they move nothing and give zeros.
 // kWith: kPlan: workgroup 0 runs the layer's plan; kLora: the adapters' part is
-// added (see add_lora).
+// added (see LoraPart), and workgroup 0 runs the plan where it is to be made.
 enum With { kNone, kPlan, kLora };
 struct Nothing {};
+struct LoraWith {
+  W4Lora lora;
+  PlanArgs plan;
+  int32_t planned;
+};
 template <With kWith>
-using with_t = std::conditional_t<kWith == kPlan, PlanArgs, std::conditional_t<kWith == kLora, W4Lora, Nothing>>;
+using with_t = std::conditional_t<kWith == kPlan, PlanArgs, std::conditional_t<kWith == kLora, LoraWith, Nothing>>;
 
 // The adapters' part of a workgroup's rows and columns, t B_s^T, is the work of
 // lora_waves more waves: what it waits for, one after the other (the rows'
 // adapters, then their B), passes while the others stream W.  8192 x 9216, one row: 9
 // us without it, 10 so, 13 - 14 where the same waves did it before, in or after their
-// own records; 16 rows of 12 adapters: 14 so, 16 - 19.
-template <int FM>
-constexpr int lora_waves = FM == 1 ? 8 : 4;  // as many as FM row tiles of W leave registers for
+// own records; 16 rows of 12 adapters: 14 so, 16 - 19.  For 33 to 64 rows, in two tiles,
+// it took as long as the product, a plan and two kernels more, or up to 1.3 of it.
+template <int FM, int FN>
+constexpr int lora_waves = FM * FN <= 3 ? 8 : 4;  // as many as the sums of W's waves leave registers for
 
 // Each distinct adapter and 16 columns are one unit, kAhead of them with their B on its
 // way at once.  A product is taken for all rows of a tile and added to those of that
@@ -346,7 +352,7 @@ struct LoraPart {
             at[i] = j < FN ? j : 0;
             us[i] = s;
             ur[i] = rk;
-            j += lora_waves<FM>;
+            j += lora_waves<FM, FN>;
           }
           if (of[0] == 0) break;
           if (vec) load_b();
@@ -360,11 +366,11 @@ struct LoraPart {
 };
 
 template <int FM, int FN, int NW, int PD, int SG, With kWith>
-__global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM> : 0))) void k_w4_split(W4GemmArgs p,
+__global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM, FN> : 0))) void k_w4_split(W4GemmArgs p,
                                                                                               with_t<kWith> with) {
   constexpr int REC = (int)w4_record(SG), KS = 4 / SG;
   constexpr int HALF = FM * 2048, XI = 2 * FM;  // x: bytes of half a record, loads of 1 KiB
-  constexpr int ALL = NW + (kWith == kLora ? lora_waves<FM> : 0);
+  constexpr int ALL = NW + (kWith == kLora ? lora_waves<FM, FN> : 0);
   constexpr int RING = NW * PD * 2 * HALF, PART = ALL * FM * FN * 1024;
   constexpr int kYounger = XI + (PD - 1) * (FN * (1 + SG) + 2 * XI) + FN * (1 + SG);
   constexpr int PLAN = kWith == kPlan ? (int)plan_detail::plan_sort_lds(plan_detail::kPlanRowBitsMax) : 0;
@@ -376,6 +382,13 @@ __global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM> : 0))) 
       return;
     }
     --bx;
+  } else if constexpr (kWith == kLora) {
+    if (with.planned && bx == 0) {
+      // by as many waves as it is made for; the others are gone before its barriers
+      if (blockIdx.y == 0 && threadIdx.x < 64 * NW) plan_detail::plan_body<64 * NW>(with.plan, smem, sizeof(smem));
+      return;
+    }
+    bx -= with.planned;
   }
   const int lane = threadIdx.x & 63, r = lane & 15, h = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -420,8 +433,8 @@ __global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM> : 0))) 
   const uint32_t xa = lds_addr(ring) + r * 128;
   if (kWith == kLora && wave >= NW) {
     if constexpr (kWith == kLora) {
-      touch(with);
-      LoraPart<FM, FN>(with, m0, n0).run(wave - NW, tot);
+      touch(with.lora);
+      LoraPart<FM, FN>(with.lora, m0, n0).run(wave - NW, tot);
     }
   } else {
 #pragma unroll
@@ -506,31 +519,24 @@ __global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM> : 0))) 
   }
 }
 
-// What goes with a launch: nothing, a plan or the adapters' part.
-struct Extra {
-  const PlanArgs *plan;
-  const W4Lora *lora;
-};
-
-constexpr int kLoraTiles = 2;  // of rows at most where the adapters' part is added: registers for twelve waves
-
 template <int FM, int FN, int NW, int PD, int SG>
-void launch_split(const W4GemmArgs &a, const Extra &x, hipStream_t st) {
-  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN) + (x.plan ? 1 : 0), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
-  if (x.plan) {
-    hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kPlan>), grid, block, 0, st, a, *x.plan);
-  } else if (x.lora) {
-    if constexpr (FM <= kLoraTiles)
-      hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kLora>), grid, dim3(64 * (NW + lora_waves<FM>)), 0, st, a, *x.lora);
-  } else {
-    hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kNone>), grid, block, 0, st, a, Nothing{});
-  }
+void launch_split(const W4GemmArgs &a, const PlanArgs *plan, hipStream_t st) {
+  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN) + (plan ? 1 : 0), (a.M + 16 * FM - 1) / (16 * FM)), block(64 * NW);
+  if (plan) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kPlan>), grid, block, 0, st, a, *plan);
+  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, SG, kNone>), grid, block, 0, st, a, Nothing{});
 }
 template <int FM, int FN, int NW, int PD>
-void launch_split(W4GemmArgs a, const Extra &x, hipStream_t st) {
-  if (a.sg == 1) launch_split<FM, FN, NW, PD, 1>(a, x, st);
-  else if (a.sg == 2) launch_split<FM, FN, NW, PD, 2>(a, x, st);
-  else launch_split<FM, FN, NW, PD, 4>(a, x, st);
+void launch_split(W4GemmArgs a, const PlanArgs *plan, hipStream_t st) {
+  if (a.sg == 1) launch_split<FM, FN, NW, PD, 1>(a, plan, st);
+  else if (a.sg == 2) launch_split<FM, FN, NW, PD, 2>(a, plan, st);
+  else launch_split<FM, FN, NW, PD, 4>(a, plan, st);
+}
+template <int FM, int FN, int NW, int PD>
+void launch_lora(const W4GemmArgs &a, const LoraWith &w, hipStream_t st) {
+  const dim3 grid((a.N + 16 * FN - 1) / (16 * FN) + w.planned), block(64 * (NW + lora_waves<FM, FN>));
+  if (a.sg == 1) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 1, kLora>), grid, block, 0, st, a, w);
+  else if (a.sg == 2) hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 2, kLora>), grid, block, 0, st, a, w);
+  else hipLaunchKernelGGL((k_w4_split<FM, FN, NW, PD, 4, kLora>), grid, block, 0, st, a, w);
 }
 
 // Rows of x past 32-bit offsets of one another (the last tokens of long
@@ -846,19 +852,19 @@ __global__ __launch_bounds__(64 * WM * WN * KG) void k_w4_tile(W4GemmArgs p, wit
 }
 
 template <int FM, int FN, int WM, int WN, int KG, int ST, int WS, int SG>
-void launch_tile(const W4GemmArgs &a, const Extra &x, hipStream_t st) {
-  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n) + (x.plan ? 1 : 0)), block(64 * WM * WN * KG);
-  if (x.plan) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, SG, kPlan>), grid, block, 0, st, a, *x.plan);
+void launch_tile(const W4GemmArgs &a, const PlanArgs *plan, hipStream_t st) {
+  const dim3 grid((unsigned)(a.tiles_m * a.tiles_n) + (plan ? 1 : 0)), block(64 * WM * WN * KG);
+  if (plan) hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, SG, kPlan>), grid, block, 0, st, a, *plan);
   else hipLaunchKernelGGL((k_w4_tile<FM, FN, WM, WN, KG, ST, WS, SG, kNone>), grid, block, 0, st, a, Nothing{});
 }
 template <int FM, int FN, int WM, int WN, int KG, int ST, int WS>
-void launch_tile(W4GemmArgs a, const Extra &x, hipStream_t st) {
+void launch_tile(W4GemmArgs a, const PlanArgs *plan, hipStream_t st) {
   constexpr int BM = 16 * FM * WM, BN = 16 * FN * WN;
   a.tiles_m = (a.M + BM - 1) / BM;
   a.tiles_n = (a.N + BN - 1) / BN;
-  if (a.sg == 1) launch_tile<FM, FN, WM, WN, KG, ST, WS, 1>(a, x, st);
-  else if (a.sg == 2) launch_tile<FM, FN, WM, WN, KG, ST, WS, 2>(a, x, st);
-  else launch_tile<FM, FN, WM, WN, KG, ST, WS, 4>(a, x, st);
+  if (a.sg == 1) launch_tile<FM, FN, WM, WN, KG, ST, WS, 1>(a, plan, st);
+  else if (a.sg == 2) launch_tile<FM, FN, WM, WN, KG, ST, WS, 2>(a, plan, st);
+  else launch_tile<FM, FN, WM, WN, KG, ST, WS, 4>(a, plan, st);
 }
 
 // ---------------------------------------------------------------- which
@@ -881,7 +887,7 @@ struct Shape {
   bool rounds;  // the weights, to bf16
   int held;     // workgroups that a CU holds
   Cost cost[3];  // groups of 128 and more, 64, 32
-  void (*launch)(W4GemmArgs, const Extra &, hipStream_t);
+  void (*launch)(W4GemmArgs, const PlanArgs *, hipStream_t);
 };
 constexpr int held(int smem, int waves) { return std::max(1, std::min(160 * 1024 / smem, 16 / waves)); }
 template <int FM, int FN, int NW, int PD>
@@ -927,17 +933,18 @@ const Shape kShapes[] = {
     tile<8, 4, 2, 4, 1, 3, 2>({1, 0.f, 6.5f, 2.68f, 0.f, 0.733f}),
 };
 
-// lora: with the adapters' part.  The shapes that add it give every row the same
-// sums as those that the product takes for as many rows.
-const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg, bool lora = false) {
+// A shape's time by the model above.
+double time_of(const Cost &c, int64_t tiles, int32_t nb) {
+  const double rounds = (double)((tiles + 256 * c.fit - 1) / (256 * c.fit)), cu = (double)((tiles + 255) / 256);
+  return c.s + rounds * (c.e + (double)c.c * nb) + (cu * c.w + (double)tiles / 256 * c.f) * nb;
+}
+
+const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
   const Shape *best = nullptr;
   double least = 0;
   for (const Shape &h : kShapes) {
-    if ((h.rounds && M <= kW4Rows) || (lora && h.bm > 16 * kLoraTiles)) continue;
-    const Cost &c = h.cost[sg >> 1];
-    const int64_t tiles = (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn);
-    const double rounds = (double)((tiles + 256 * c.fit - 1) / (256 * c.fit)), cu = (double)((tiles + 255) / 256);
-    const double t = c.s + rounds * (c.e + (double)c.c * nb) + (cu * c.w + (double)tiles / 256 * c.f) * nb;
+    if (h.rounds && M <= kW4Rows) continue;  // a layer of so few rows takes the others
+    const double t = time_of(h.cost[sg >> 1], (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn), nb);
     if (best == nullptr || t < least) {
       best = &h;
       least = t;
@@ -945,6 +952,58 @@ const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg, bool lora = f
   }
   return *best;
 }
+
+// The same with the adapters' part, which leaves a CU room for one workgroup.  Every
+// row has the sums that the shapes above give it.  Fits of the whole layer's times at
+// 1 to 32 rows, ranks 16 and 64, d x k of 32768 x 8192, 32768 x 4096, 20480 x 2048,
+// 16384 x 4096, 10240 x 8192 and below, good to 6 - 15% (ranks and adapters are not
+// in them); the choice takes 1.02 of the best of ten shapes' time, on the mean.
+struct LoraShape {
+  int bm, bn;
+  Cost cost[3];
+  void (*launch)(const W4GemmArgs &, const LoraWith &, hipStream_t);
+};
+template <int FM, int FN, int NW, int PD>
+constexpr LoraShape lora(Cost g128, Cost g64, Cost g32) {
+  return {16 * FM, 16 * FN, {g128, g64, g32}, launch_lora<FM, FN, NW, PD>};
+}
+const LoraShape kLoraShapes[] = {
+    lora<1, 1, 8, 2>({1, 9.8f, 2.71f, 0.f, 0.f, 0.0372f},
+                     {1, 9.95f, 2.64f, 0.f, 0.f, 0.0435f},
+                     {1, 10.1f, 2.58f, 0.f, 0.f, 0.0497f}),
+    lora<1, 2, 8, 1>({1, 10.2f, 1.61f, 0.0062f, 0.f, 0.0759f},
+                     {1, 9.54f, 1.65f, 0.0286f, 0.f, 0.071f},
+                     {1, 8.87f, 1.68f, 0.051f, 0.f, 0.0662f}),
+    lora<1, 3, 8, 1>({1, 7.78f, 2.74f, 0.056f, 0.f, 0.0396f},
+                     {1, 7.59f, 2.37f, 0.0918f, 0.f, 0.0387f},
+                     {1, 7.4f, 2.f, 0.128f, 0.f, 0.0377f}),
+    lora<1, 4, 8, 1>({1, 7.12f, 6.04f, 0.0324f, 0.f, 0.0594f},
+                     {1, 8.35f, 4.16f, 0.0764f, 0.f, 0.0954f},
+                     {1, 9.57f, 2.27f, 0.12f, 0.f, 0.131f}),
+    lora<2, 2, 8, 1>({1, 7.62f, 5.67f, 0.0455f, 0.f, 0.0573f},
+                     {1, 7.51f, 5.54f, 0.0705f, 0.f, 0.0506f},
+                     {1, 7.4f, 5.4f, 0.0954f, 0.f, 0.0439f}),
+    lora<2, 3, 8, 1>({1, 8.36f, 6.28f, 0.064f, 0.f, 0.0595f},
+                     {1, 8.57f, 5.7f, 0.102f, 0.f, 0.0601f},
+                     {1, 8.79f, 5.12f, 0.14f, 0.f, 0.0607f}),
+    lora<2, 4, 8, 1>({1, 9.26f, 7.45f, 0.0585f, 0.f, 0.12f},
+                     {1, 8.9f, 7.35f, 0.105f, 0.f, 0.12f},
+                     {1, 8.55f, 7.26f, 0.151f, 0.f, 0.12f}),
+};
+const LoraShape &best_lora(int64_t M, int64_t N, int32_t nb, int32_t sg) {
+  const LoraShape *best = nullptr;
+  double least = 0;
+  for (const LoraShape &h : kLoraShapes) {
+    if (h.bm != (M > 16 ? 32 : 16)) continue;  // W once
+    const double t = time_of(h.cost[sg >> 1], (N + h.bn - 1) / h.bn, nb);
+    if (best == nullptr || t < least) {
+      best = &h;
+      least = t;
+    }
+  }
+  return *best;
+}
+static_assert(kW4Rows == 32, "the rows of a tile");
 
 // slabs whose grids stay far below what a launch takes
 constexpr int64_t kSlabM = int64_t(1) << 18, kSlabN = int64_t(1) << 20;
@@ -986,10 +1045,22 @@ bool gemm_w4_runs_plan(const W4GemmArgs &a) {
   const int64_t tiles = (int64_t)((a.M + h.bm - 1) / h.bm) * ((a.N + h.bn - 1) / h.bn);
   return tiles % (256 * h.held) != 0;
 }
+bool gemm_w4_lora_runs_plan(const W4GemmArgs &a) {
+  const int bn = best_lora(a.M, a.N, a.nb, a.sg).bn;
+  return (a.N + bn - 1) / bn % 256 != 0;
+}
 
-hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs *plan, const W4Lora *lora) {
+hipError_t launch_gemm_w4_lora(const W4GemmArgs &a, const W4Lora &l, hipStream_t st, const PlanArgs *plan) {
+  if (!gemm_w4_adds_lora(a)) return hipErrorInvalidValue;
+  LoraWith w{l, {}, plan != nullptr};
+  if (plan) w.plan = *plan;
+  best_lora(a.M, a.N, a.nb, a.sg).launch(a, w, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs *plan) {
   const bool far = far_rows(all);
-  if ((plan && !gemm_w4_runs_plan(all)) || (lora && !gemm_w4_adds_lora(all))) return hipErrorInvalidValue;
+  if (plan && !gemm_w4_runs_plan(all)) return hipErrorInvalidValue;
   for (int64_t m0 = 0; m0 < all.M; m0 += kSlabM)
     for (int64_t n0 = 0; n0 < all.N; n0 += kSlabN) {
       W4GemmArgs a = all;
@@ -999,7 +1070,7 @@ hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs 
       a.w += n0 / 16 * a.nb * w4_record(a.sg);
       a.y += m0 * a.ldy + n0;
       if (!far) {
-        best_of(a.M, a.N, a.nb, a.sg, lora != nullptr).launch(a, Extra{plan, lora}, st);
+        best_of(a.M, a.N, a.nb, a.sg).launch(a, plan, st);
       } else {
         const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
         if (a.sg == 1) hipLaunchKernelGGL(k_w4_far<1>, grid, dim3(256), 0, st, a);

@@ -1,4 +1,4 @@
-// w4_layer.hip -- the 4-bit layer for at most 64 rows (include/lora_w4.h): what
+// w4_layer.hip -- the 4-bit layer for at most 32 rows (include/lora_w4.h): what
 // goes ahead of the product that adds the adapters' part itself (w4.hip).
 //
 // With so few rows a plan has little to sort, and its launch, and the fork and

@@ -348,7 +348,14 @@ def test_layer(case, pools):
         assert chk["n_bad_ids"] == chk["n_bad_ranks"] == chk["n_bad_pages"] == chk["n_sync_expired"] == 0
 
 
-FEW = [  # M, k, ds, group, max_rank, ranks: at and around 64 rows
+FEW = [  # M, k, ds, group, max_rank, ranks: at and around 32 and 64 rows
+    (32, 520, (5, 7, 3, 40), 32, 256, [200]),
+    (32, 264, (48, 17), 64, 64, list(range(1, 33))),
+    (19, 1288, (33,), 128, 12, [12, 7, 1]),
+    (9, 4104, (16, 300), 128, 96, [96, 8, 64, 72, 0]),
+    (16, 136, (300, 4500), 128, 20, [20, 16, 3]),
+    (30, 1032, (8200,), 64, 8, [8, 3]),
+    (33, 264, (48, 17), 64, 64, list(range(1, 34))),
     (64, 520, (5, 7, 3, 40), 32, 256, [200]),             # one adapter's rows; slices inside 16 columns
     (64, 264, (48, 17), 64, 64, list(range(1, 65))),      # an adapter for every row
     (33, 1288, (33,), 128, 12, [12, 7, 1]),               # B's rows no whole vectors
@@ -405,6 +412,33 @@ def test_layer_keeps_an_adapters_nan_to_its_rows(M):
     y = run()
     assert torch.equal(y[other], clean[other])
     assert not torch.isfinite(y[~other].float()).any()
+
+
+@pytest.mark.parametrize("d", [64, 16 * 512, 16 * 768])  # tiles that leave room beside them, and do not
+@pytest.mark.parametrize("M", [1, 16, 40, 64, 150])
+def test_plan_is_left_and_reused(M, d):
+    """The plan a call makes serves a dense layer of the same rows, and the
+    other way about; a call that reuses one leaves it as it is."""
+    k, ranks = 128, [4, 16, 9, 0, 7]
+    say("w4 plan %d %d" % (M, d))
+    q, s, z = R.weight(3, d, k, 64)
+    W = device_weight(q, s, z, 64)
+    Wd = lr.lora_w4_dequantize(W)
+    slices = device_slices([adapter_set(1, 5, 16, k, d, ranks)], ranks, [1.0, 2.0, 0.5, 1.0, 3.0], (d,), k, 16)
+    ids = torch.from_numpy(np.random.default_rng(M).integers(-2, 7, M).astype(np.int32)).cuda()
+    x = loud(4, M, k).cuda()
+    n = max(lr.workspace_bytes_sliced_w4(M, k, slices), lr.workspace_bytes_sliced(M, k, BF, slices))
+    new = lambda: torch.zeros(n, dtype=torch.uint8, device="cuda")
+    four = lambda ws, flags=0: lr.lora_linear_sliced_w4(x, W, slices, ids, workspace=ws, flags=flags)
+    dense = lambda ws, flags=0: lr.lora_linear_sliced(x, Wd, slices, ids, workspace=ws, flags=flags)
+    ws, other = new(), new()
+    y = four(ws)
+    counts = lr.lora_check(ws)
+    assert torch.equal(dense(ws, lr.FLAG_REUSE_PLAN), dense(other))
+    assert {n: v for n, v in lr.lora_check(other).items()} == counts
+    assert torch.equal(four(other, lr.FLAG_REUSE_PLAN), y)
+    assert torch.equal(dense(other, lr.FLAG_REUSE_PLAN), dense(new()))
+    assert torch.equal(four(ws, lr.FLAG_REUSE_PLAN), y)
 
 
 @pytest.mark.parametrize("pools", [False, True])
