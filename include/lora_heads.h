@@ -54,8 +54,9 @@ typedef struct lora_rope {
  * elements; head_dim 1 .. 1024, n_heads 1 .. 65535, strides below 2^40;
  * rows and heads of a tensor must not overlap one another: ld_head >=
  * head_dim and ld_row >= (n_heads - 1) ld_head + head_dim (the first only
- * where n_heads > 1, the second where M > 1).  Norms and angles are computed
- * in 64 bits, products in 32; each output is rounded once.  A row whose
+ * where n_heads > 1, the second where M > 1).  Sums of squares and angles
+ * are computed in 64 bits, the values in fp32 (two roundings of the norm, three
+ * of the rotation); each output is rounded once from there.  A row whose
  * position is negative (padding) is left as it is in both outputs.  The
  * angle is exact to 2^-50 of itself: to fp32's last bit for positions below
  * 2^26.  A q or k `out` over an input other than its own x, or over the other

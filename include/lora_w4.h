@@ -102,8 +102,11 @@ size_t lora_workspace_bytes_sliced_w4(int64_t max_rows, int64_t k, int32_t n_sli
 /*
  * lora_linear_sliced over such a base weight (bf16 x, y, adapters): W stacks
  * the slices' base weights by rows.  Everything else as in
- * lora_linear_sliced.  y must not overlap x, W or the workspace
- * (LORA_ERR_ARG).
+ * lora_linear_sliced.  Rows without an adapter are lora_gemm_w4's, bit for
+ * bit (up to 8192 rows, which one plan holds); up to 32 rows (but by LORA_PATH_GATHER) need no plan, round y once and
+ * keep 16 bits of each rank's product between A and B; they leave a plan for
+ * others unless LORA_FLAG_REUSE_PLAN is given.  y must not overlap x, W or
+ * the workspace (LORA_ERR_ARG).
  */
 lora_status_t lora_linear_sliced_w4(int64_t M, int64_t k, const void *x, int64_t ldx,
                                     const lora_w4_t *W, int32_t n_slices,

@@ -73,7 +73,8 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4Args a) {
 
 // A workgroup reads kDqRecords records of 16 rows back; of each, a thread takes
 // a dword of codes (eight columns of a row) and sixteen threads a row's 128
-// columns.  All of a thread's loads go ahead of its stores.
+// columns.  All of a thread's loads go ahead of its stores.  Bound by its bytes:
+// 9216 x 8192 to bf16 45 us, 4.2 TB/s.
 constexpr int kDqRecords = 8;
 template <typename T>
 __global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, int32_t per_row) {
@@ -166,6 +167,12 @@ __device__ __forceinline__ void read_half(uint32_t a0, uint32_t a1, u32x4_t (&x)
 // both PD records ahead.  The waves' sums meet in LDS at the end, in their order.
 // Loads past the end of a wave's records, of x's rows and of its columns are
 // past their buffer: they move nothing and give zeros.
+//
+// 1 x 9216 x 8192, groups of 128: 8.5 us, bound by W's bytes (4.7 TB/s, most of them from
+// the last-level cache); 7 x 4999 x 5000, groups of 32: 7.0, its records' latencies
+// one after the other; 256 x 4096 x 4096: 15.2, unpacking and scaling between the products
+// (matrix units busy 32%).  Eight waves a tile: sixteen took the same within 1%.
+//
 // kWith: kPlan: workgroup 0 runs the layer's plan; kLora: the adapters' part is
 // added (see LoraPart), and workgroup 0 runs the plan where it is to be made.
 enum With { kNone, kPlan, kLora };
@@ -650,6 +657,11 @@ struct WTile {
   static_assert((ST - 1) * XL + ST / 2 * WL < 64, "vmcnt");
 };
 
+// 8192 x 4096 x 4096 (groups of 64, 256 x 256 tiles): 236 us, 1.16 PFLOP/s, against 202
+// at the library's bf16 rate; 512 x 9216 x 8192 (groups of 128, 128 x 160): 85 - 95.  Unpacking
+// bounds both: it takes issue slots that other waves' matrix instructions do not
+// fill (two VALU instructions behind one are free, a third takes a quarter of it more).
+//
 // The tile of this workgroup: each XCD takes a contiguous run of tiles, bands
 // of eight row tiles down, then across.
 __device__ __forceinline__ void tile_of(const W4GemmArgs &p, uint32_t b, int &tm, int &tn) {
