@@ -204,6 +204,17 @@ def test_product_of_far_rows():
     assert torch.equal(y.cpu(), want)
 
 
+@pytest.mark.parametrize("M,d", [((1 << 18) + 70, 24), (3, (1 << 20) + 40), (70, (1 << 20) + 17)])
+def test_product_past_a_slab(M, d):
+    """More rows, or columns, than one launch takes."""
+    k = 64
+    q, s, z = R.weight(1, d, k, 32, exact=True)
+    x = whole(2, M, k)
+    y = lr.lora_gemm_w4(x.cuda(), device_weight(q, s, z, 32))
+    want = (x.cuda().float() @ torch.from_numpy(R.dequant(q, s, z, 32)).float().cuda().T).to(BF)  # exact in fp32
+    assert torch.equal(y, want)
+
+
 def test_empty_batch():
     q, s, z = R.weight(2, 20, 256, 128)
     W = device_weight(q, s, z, 128)
@@ -461,6 +472,62 @@ def test_layer_of_whole_numbers_exactly(M, pools):
     want = layer_ref(x, Wd, ds, sets, ranks, scales.astype(np.float64), ids)
     base = x.double().numpy() @ Wd.T
     assert (np.abs(y - want) <= 2.0 ** -8 * (np.abs(want) + np.abs(base))).all()
+
+
+def check_whole_layer(x, Wq, ds, sets, ranks, scales, ids, group, y):
+    """As in test_layer_of_whole_numbers_exactly."""
+    Wd = R.dequant(*Wq, group)
+    want = layer_ref(x, Wd, ds, sets, ranks, scales, ids)
+    base = x.double().numpy() @ Wd.T
+    got = y.cpu().double().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -8 * (np.abs(want) + np.abs(base))).all()
+
+
+@pytest.mark.parametrize("pools", [False, True])
+@pytest.mark.parametrize("M", [1, 5, 20, 100])
+def test_layer_of_views(M, pools):
+    """x and y are columns of wide buffers, y's at an odd place; nothing past
+    a row is written or read into the sums."""
+    k, ds, group, ranks = 904, (40, 37), 128, [8, 3]
+    q = R.weight(M, sum(ds), k, group, exact=True)
+    sets = [adapter_set(30 + i, 2, 8, k, d, ranks, exact=True) for i, d in enumerate(ds)]
+    ids = (np.arange(M) % 3 - 1).astype(np.int32)
+    x = whole(M, M, k)
+    wide = torch.full((M, k + 40), float("nan"), dtype=BF, device="cuda")
+    wide[:, 16:16 + k] = x.cuda()
+    out = torch.full((M, sum(ds) + 9), 5.0, dtype=BF, device="cuda")
+    lr.lora_linear_sliced_w4(wide[:, 16:16 + k], device_weight(*q, group),
+                             device_slices(sets, ranks, [1.0, 2.0], ds, k, 8, pools), torch.from_numpy(ids).cuda(),
+                             y=out[:, 3:3 + sum(ds)])
+    check_whole_layer(x, q, ds, sets, ranks, [1.0, 2.0], ids, group, out[:, 3:3 + sum(ds)])
+    assert bool((out[:, :3] == 5).all()) and bool((out[:, 3 + sum(ds):] == 5).all())
+
+
+@pytest.mark.parametrize("M,far", [(3, 1 << 31), (30, 1 << 24), (100, 1 << 23)])
+def test_layer_of_far_rows(M, far):
+    k, d, ranks = 256, 40, [8, 3]
+    q = R.weight(9, d, k, 64, exact=True)
+    sets = [adapter_set(30, 2, 8, k, d, ranks, exact=True)]
+    ids = (np.arange(M) % 3 - 1).astype(np.int32)
+    x = whole(5, M, k)
+    view = torch.empty((M - 1) * far + k, dtype=BF, device="cuda").as_strided((M, k), (far, 1))
+    view.copy_(x.cuda())
+    y = lr.lora_linear_sliced_w4(view, device_weight(*q, 64), device_slices(sets, ranks, [1.0, 2.0], (d,), k, 8),
+                                 torch.from_numpy(ids).cuda())
+    check_whole_layer(x, q, (d,), sets, ranks, [1.0, 2.0], ids, 64, y)
+
+
+@pytest.mark.parametrize("M", [2, 40])
+def test_layer_past_a_slab(M):
+    """More columns than one launch of the product takes."""
+    k, d, ranks = 64, (1 << 20) + 40, [4, 2]
+    q = R.weight(1, d, k, 64, exact=True)
+    sets = [adapter_set(3, 2, 8, k, d, ranks, exact=True)]
+    ids = (np.arange(M) % 3 - 1).astype(np.int32)
+    x = whole(3, M, k)
+    y = lr.lora_linear_sliced_w4(x.cuda(), device_weight(*q, 64), device_slices(sets, ranks, [1.0, 2.0], (d,), k, 8),
+                                 torch.from_numpy(ids).cuda())
+    check_whole_layer(x, q, (d,), sets, ranks, [1.0, 2.0], ids, 64, y)
 
 
 @pytest.mark.parametrize("M", [6, 100])
