@@ -1260,8 +1260,12 @@ def lora_linear_sliced_w4(x: torch.Tensor, W: W4, slices, adapter_ids: torch.Ten
         raise ValueError("W must stack the slices' weights on x's device: [%d, %d] expected" % (d_total, k))
     _check_layer(slices, adapter_ids, M, k, bf, device)
     if y is None:
-        y = _empty((M, d_total), bf, device, stream)
-    yp, ldy = _matrix(y, "y", (M, d_total), bf, device)
+        ldy = d_total
+        y = (torch.empty_strided((M, ldy), (ldy, 1), dtype=bf, device=device) if stream is None
+             else _empty((M, ldy), bf, device, stream))
+        yp = y.data_ptr()
+    else:
+        yp, ldy = _matrix(y, "y", (M, d_total), bf, device)
     arr = _slice_array(slices)
     if workspace is None:  # needs no initialisation, and lora_check sees it no more
         n = lib.lora_workspace_bytes_sliced_w4(M, k, len(slices), arr)
@@ -1281,19 +1285,19 @@ class Rope:
     in radians a position, pairs (i, i + rot_dim / 2) or, interleaved, (2i,
     2i + 1), and a factor on cos and sin."""
 
-    __slots__ = ("inv_freq", "rot_dim", "interleaved", "scale", "device", "pointer")
+    __slots__ = ("inv_freq", "rot_dim", "interleaved", "scale", "index", "pointer")
 
     def __init__(self, inv_freq: torch.Tensor, interleaved: bool = False, scale: float = 1.0):
-        self.pointer, self.device = _dev(inv_freq, "inv_freq", torch.float32), inv_freq.device
+        self.pointer, self.index = _dev(inv_freq, "inv_freq", torch.float32), inv_freq.get_device()
         if inv_freq.dim() != 1:
             raise ValueError("inv_freq must be 1-D")
         self.inv_freq, self.rot_dim = inv_freq, 2 * inv_freq.numel()
         self.interleaved, self.scale = bool(interleaved), float(scale)
 
 
-def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, device, stream):
+def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, index, stream):
     """(descriptor, output) of the heads of q or k, whose own type and device
-    have been checked."""
+    (by its index) have been checked."""
     M, H, D = shape
     lr, lh, unit = x.stride()
     if unit != 1 and D > 1:
@@ -1303,18 +1307,25 @@ def _head_set(x: torch.Tensor, name: str, weight, out, shape, dtype, device, str
     else:
         if weight.dtype is not dtype:
             raise TypeError("%s's weight must share its dtype" % name)
-        if weight.device != device or weight.shape != shape[2:] or not weight.is_contiguous():
+        if weight.get_device() != index or weight.dim() != 1 or weight.numel() != D or not weight.is_contiguous():
             raise ValueError("%s's weight must be a contiguous [%d] tensor on its device" % (name, D))
         wp = weight.data_ptr()
     if out is None:
-        lor, loh = H * D, D
-        # (by strides: 1.3 us a call against torch.empty's 2.1)
-        out = (torch.empty_strided(shape, (lor, loh, 1), dtype=dtype, device=device) if stream is None
-               else _empty(shape, dtype, device, stream))
+        # (a call's own time on the host is most of a small one's: 1.1 us so and 1.4 by
+        # strides, against torch.empty's 2.1)
+        if stream is not None:
+            out = _empty(shape, dtype, x.device, stream)
+            lor, loh = H * D, D
+        elif x.is_contiguous():
+            out = torch.empty_like(x)
+            lor, loh = lr, lh
+        else:
+            lor, loh = H * D, D
+            out = torch.empty_strided(shape, (lor, loh, 1), dtype=dtype, device=x.device)
     else:
         if out.dtype is not dtype:
             raise TypeError("%s's output must share its dtype" % name)
-        if out.device != device or out.shape != shape:
+        if out.get_device() != index or out.shape != shape:
             raise ValueError("%s's output must be [%d, %d, %d] on its device" % (name, M, H, D))
         lor, loh, unit = out.stride()
         if unit != 1 and D > 1:
@@ -1335,34 +1346,35 @@ def lora_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None,
     two outputs.  q_out and k_out may be q and k themselves.  Rows with a
     negative position are left as they are: of outputs made here, unset."""
     lib = _lib or load_library()
-    dtype, device, shape = q.dtype, q.device, q.shape
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
     dt = _DTYPES.get(dtype)
     if dt is None:
         raise TypeError("unsupported dtype %s (float32 or bfloat16)" % dtype)
-    if len(shape) != 3 or device.type != "cuda":
+    if len(shape) != 3 or not q.is_cuda:
         raise ValueError("q must be a 3-D device tensor")
     M, _, D = shape
-    cq, q_out = _head_set(q, "q", q_weight, q_out, shape, dtype, device, stream)
+    cq, q_out = _head_set(q, "q", q_weight, q_out, shape, dtype, index, stream)
     ck = cr = None
     if k is not None:
         ks = k.shape
-        if len(ks) != 3 or ks[0] != M or ks[2] != D or k.device != device:
+        if len(ks) != 3 or ks[0] != M or ks[2] != D or k.get_device() != index:
             raise ValueError("k must be [%d, heads, %d] on q's device" % (M, D))
         if k.dtype is not dtype:
             raise TypeError("k must share q's dtype")
-        ck, k_out = _head_set(k, "k", k_weight, k_out, ks, dtype, device, stream)
+        ck, k_out = _head_set(k, "k", k_weight, k_out, ks, dtype, index, stream)
         ck = _byref(ck)
     if rope is not None:
         if positions is None:
             raise ValueError("a rotation needs positions")
         if positions.dtype is not torch.int64:
             raise TypeError("positions must be int64")
-        if positions.shape != shape[:1] or positions.device != device or not positions.is_contiguous():
+        if (positions.dim() != 1 or positions.numel() != M or positions.get_device() != index
+                or not positions.is_contiguous()):
             raise ValueError("positions must be a contiguous [%d] tensor on q's device" % M)
-        if rope.device != device:
+        if rope.index != index:
             raise ValueError("inv_freq must be a tensor on q's device")
         cr = _byref(_CRope(positions.data_ptr(), rope.pointer, rope.rot_dim, rope.interleaved, rope.scale))
-    _on(device, stream, lib.lora_qk_norm_rope, "lora_qk_norm_rope", dt, M, D, eps, _byref(cq), ck, cr)
+    _on(q.device, stream, lib.lora_qk_norm_rope, "lora_qk_norm_rope", dt, M, D, eps, _byref(cq), ck, cr)
     return q_out, k_out
 
 
