@@ -158,21 +158,6 @@ __device__ __forceinline__ void read_half(uint32_t a0, uint32_t a1, u32x4_t (&x)
                    "=&v"(x[1][2]), "=&v"(x[1][3]) : "v"(a0), "v"(a1) : "memory");
 }
 
-// A workgroup takes 16 FM rows of x and 16 FN of W, each of its NW waves every
-// NW-th record of k.  No wave shares an operand with another, so nothing waits
-// but for its own loads, and the waves of a SIMD drift apart: one unpacks while
-// the other multiplies.  W's records go straight to registers, x's rows by
-// direct loads through the wave's own part of LDS (fragments read from memory
-// would touch sixteen half lines an instruction: 54 cycles of a CU against 35),
-// both PD records ahead.  The waves' sums meet in LDS at the end, in their order.
-// Loads past the end of a wave's records, of x's rows and of its columns are
-// past their buffer: they move nothing and give zeros.
-//
-// 1 x 9216 x 8192, groups of 128: 8.5 us, bound by W's bytes (4.7 TB/s, most of them from
-// the last-level cache); 7 x 4999 x 5000, groups of 32: 7.0, its records' latencies
-// one after the other; 256 x 4096 x 4096: 15.2, unpacking and scaling between the products
-// (matrix units busy 32%).  Eight waves a tile: sixteen took the same within 1%.
-//
 // kWith: kPlan: workgroup 0 runs the layer's plan; kLora: the adapters' part is
 // added (see LoraPart), and workgroup 0 runs the plan where it is to be made.
 enum With { kNone, kPlan, kLora };
@@ -372,6 +357,20 @@ struct LoraPart {
   }
 };
 
+// A workgroup takes 16 FM rows of x and 16 FN of W, each of its NW waves every
+// NW-th record of k.  No wave shares an operand with another, so nothing waits
+// but for its own loads, and the waves of a SIMD drift apart: one unpacks while
+// the other multiplies.  W's records go straight to registers, x's rows by
+// direct loads through the wave's own part of LDS (fragments read from memory
+// would touch sixteen half lines an instruction: 54 cycles of a CU against 35),
+// both PD records ahead.  The waves' sums meet in LDS at the end, in their order.
+// Loads past the end of a wave's records, of x's rows and of its columns are
+// past their buffer: they move nothing and give zeros.
+//
+// 1 x 9216 x 8192, groups of 128: 8.5 us, bound by W's bytes (4.7 TB/s, most of them from
+// the last-level cache); 7 x 4999 x 5000, groups of 32: 7.0, its records' latencies
+// one after the other; 256 x 4096 x 4096: 15.2, unpacking and scaling between the products
+// (matrix units busy 32%).  Eight waves a tile: sixteen took the same within 1%.
 template <int FM, int FN, int NW, int PD, int SG, With kWith>
 __global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM, FN> : 0))) void k_w4_split(W4GemmArgs p,
                                                                                               with_t<kWith> with) {
