@@ -237,8 +237,10 @@ struct LoraPart {
       }
       return;
     }
-    // lanes with no rank load the pool's first bytes; places in 16 bytes
-    const uint32_t k8 = (uint32_t)ar.k, shift = ar.page_shift - 4, mask = (uint32_t)(ar.page_bytes >> 4) - 1;
+    // Lanes with no rank load the pool's first bytes.  Places in 16 bytes: all are below
+    // 2^30 (256 ranks of 2^24 + 2^20 columns), so pages of 2^31 of them and more have
+    // page 0 alone -- by a shift of 31, as one by 32 or more is taken modulo 32.
+    const uint32_t k8 = (uint32_t)ar.k, shift = min(ar.page_shift - 4, 31), mask = (uint32_t)(ar.page_bytes >> 4) - 1;
     uint32_t off[kAhead][2];
     int32_t page[kAhead][2];
 #pragma unroll

@@ -1,0 +1,57 @@
+"""The 4-bit weight and its layer at the ends of the ranges that the checks of
+arguments accept, bit for bit (w4_exact: every sum is exact)."""
+import numpy as np
+import pytest
+import torch
+
+import lora_row_adapter_amd as lr
+import w4_exact as E
+from gpu_helpers import say
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible: the gpu tests need an MI355X")
+    torch.cuda.set_device(0)
+    lr.load_library()
+    yield
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()  # the buffers here are of many GiB
+
+
+def test_pages_past_32_bits():
+    """Adapters in pages of 32 and of 64 GiB: places in them, counted in 16
+    bytes, are shifted by 31 and by 32 bits."""
+    k, ds, group, R = 264, (48, 40), 64, 16
+    W = E.Weight(1, sum(ds), k, group)
+    Wp = lr.lora_w4_pack(W.packed(), W.s, k, group, zeros=W.z)
+    dense = W.dense()
+    pool = torch.empty(1 << 36, dtype=torch.uint8, device="cuda")
+    for page, ranks in ((1 << 35, [16, 8]), (1 << 36, [16])):
+        S = len(ranks)
+        sets = [E.adapters(10 + i, S, R, k, d, ranks) for i, d in enumerate(ds)]
+        scales = [2.0, 0.5][:S]
+        rk = torch.tensor(ranks, dtype=torch.int32).cuda()
+        sc = torch.tensor(scales, dtype=F32).cuda()
+        for M in (1, 9, 30, 50):
+            say("w4 layer, pages of 2^%d bytes, %d rows" % (page.bit_length() - 1, M))
+            ids = np.arange(M) % (S + 1) - (M > 1)
+            ids_d = torch.from_numpy(ids.astype(np.int32)).cuda()
+            x = E.rows(M, M, k)
+            for n in range(len(ds)):  # one slice's adapters fill the pool at a time
+                A, B = sets[n]
+                table = torch.tensor([[S - 1 - i] for i in range(S)], dtype=torch.int32).cuda()
+                for i, r in enumerate(ranks):
+                    raw = torch.cat([A[i, :r].reshape(-1), B[i, :, :r].reshape(-1)]).view(torch.uint8)
+                    at = (S - 1 - i) * page
+                    pool[at:at + raw.numel()] = raw
+                ad = [lr.Adapters.slots(a, b, rk) for a, b in sets]
+                ad[n] = lr.Adapters.paged(pool, table, rk, page, R)
+                y = lr.lora_linear_sliced_w4(x, Wp, [lr.Slice(d, a, sc) for d, a in zip(ds, ad)], ids_d)
+                want, _ = E.layer(x, dense, ds, sets, ranks, scales, ids, twice=M > 32)
+                assert torch.equal(y, want)
