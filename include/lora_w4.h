@@ -72,13 +72,14 @@ lora_status_t lora_w4_dequantize(lora_dtype_t dtype, int64_t d, int64_t k, const
 
 /*
  * y = x W^T: x bf16 [M, k] (k, ldx multiples of 8, 16-byte aligned), y bf16
- * [M, d] (ldy >= d).  Up to some hundred rows codes meet x exactly, and each
- * group's sum is scaled and added in fp32; past that the weights are rounded to
- * bf16, once each, ahead of the product (which of the two is a matter of the
- * sizes alone: lora_test_gemm_w4_shape).  y is rounded once.  Sums that leave
- * fp32's range on the way (|x| past 2^120 or so) and infinities in x may become
- * NaN in their row.  Deterministic: the summation order depends on the sizes
- * alone.  y must not overlap x or W (LORA_ERR_ARG).
+ * [M, d] (ldy >= d).  Up to a number of rows that the weight's sizes alone set
+ * (32 at least, 64 to some hundred for a model's: lora_test_gemm_w4_shape)
+ * codes meet x exactly, and each group's sum is scaled and added in fp32; past
+ * it the weights are rounded to bf16, once each (by 2^-8 of a weight at most),
+ * ahead of the product.  y is rounded once.  Sums that leave fp32's range on the
+ * way (|x| past 2^120 or so) and infinities in x may become NaN in their row.
+ * Deterministic: the summation order depends on the sizes alone.  y must not
+ * overlap x or W (LORA_ERR_ARG).
  */
 lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64_t ldx,
                            const lora_w4_t *W, void *y, int64_t ldy, void *stream);
@@ -101,12 +102,13 @@ size_t lora_workspace_bytes_sliced_w4(int64_t max_rows, int64_t k, int32_t n_sli
 
 /*
  * lora_linear_sliced over such a base weight (bf16 x, y, adapters): W stacks
- * the slices' base weights by rows.  Everything else as in
- * lora_linear_sliced.  Rows without an adapter are lora_gemm_w4's, bit for
- * bit (up to 8192 rows, which one plan holds); up to 32 rows (but by LORA_PATH_GATHER) need no plan, round y once and
- * keep 16 bits of each rank's product between A and B; they leave a plan for
- * others unless LORA_FLAG_REUSE_PLAN is given.  y must not overlap x, W or
- * the workspace (LORA_ERR_ARG).
+ * the slices' base weights by rows.  Everything else as in lora_linear_sliced.
+ * Rows without an adapter are lora_gemm_w4's, bit for bit (up to 8192 rows,
+ * which one plan holds).  Up to 32 rows (but by LORA_PATH_GATHER) need no plan,
+ * round y once and keep 16 bits of each rank's product between A and B; they
+ * leave a plan for others unless LORA_FLAG_REUSE_PLAN is given.  More rows round
+ * the base product to y and then its sum with the adapters' part, as the other
+ * layers do.  y must not overlap x, W or the workspace (LORA_ERR_ARG).
  */
 lora_status_t lora_linear_sliced_w4(int64_t M, int64_t k, const void *x, int64_t ldx,
                                     const lora_w4_t *W, int32_t n_slices,

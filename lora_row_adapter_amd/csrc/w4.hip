@@ -952,18 +952,57 @@ double time_of(const Cost &c, int64_t tiles, int32_t nb) {
   return c.s + rounds * (c.e + (double)c.c * nb) + (cu * c.w + (double)tiles / 256 * c.f) * nb;
 }
 
-const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
+// slabs whose grids stay far below what a launch takes
+constexpr int64_t kSlabM = int64_t(1) << 18, kSlabN = int64_t(1) << 20;
+
+// The shape that takes least of those that round the weights, or of the others.
+const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg, bool rounds, double *time) {
   const Shape *best = nullptr;
-  double least = 0;
   for (const Shape &h : kShapes) {
-    if (h.rounds && M <= kW4Rows) continue;  // a layer of so few rows takes the others
+    if (h.rounds != rounds) continue;
     const double t = time_of(h.cost[sg >> 1], (M + h.bm - 1) / h.bm * ((N + h.bn - 1) / h.bn), nb);
-    if (best == nullptr || t < least) {
+    if (best == nullptr || t < *time) {
       best = &h;
-      least = t;
+      *time = t;
     }
   }
   return *best;
+}
+
+// The rows from which on a product over a weight of these sizes rounds the weights:
+// the first number at which that is faster by the model, though with a few more it
+// may not be, so that what a row's values are rounded to does not go back and forth
+// with the rows beside it.  Never up to kW4Rows, which the layer's own shapes take.
+// Sought in steps of the smallest tile's rows, past 512 in steps of 1/16, once for
+// sizes that are not among a thread's last 16 (5 us; else as long as one shape's time).
+// Next to the faster of both everywhere, at 19 weights and 33 to 8192 rows: 1.0001
+// of the time by the model on the mean, 1.08 at most.  Measured where it decides, groups
+// of 128: 9216 x 8192, 193 rows 58.5 us against 53.1, 256 rows 59.2 against 60.1; 5120 x
+// 5120, 400 rows 38.4 against 42.7; 1024 x 8192, 2100 rows 60.3 against 62.5.
+int64_t rounded_from(int64_t N, int32_t nb, int32_t sg) {
+  struct Seen {
+    int64_t N;
+    int32_t nb, sg;
+    int64_t from;
+  };
+  thread_local Seen seen[16];
+  Seen &e = seen[(N / 16 + 5 * nb + sg) % 16];
+  if (e.N != N || e.nb != nb || e.sg != sg) {
+    int64_t m = kW4Rows + 1;
+    for (; m <= kSlabM; m += std::max<int64_t>(16, m / 256 * 16)) {
+      double exact, rounded;
+      best_of(m, N, nb, sg, false, &exact);
+      best_of(m, N, nb, sg, true, &rounded);
+      if (rounded < exact) break;
+    }
+    e = Seen{N, nb, sg, m <= kSlabM ? m : INT64_MAX};
+  }
+  return e.from;
+}
+
+const Shape &best_of(int64_t M, int64_t N, int32_t nb, int32_t sg) {
+  double t;
+  return best_of(M, N, nb, sg, M >= rounded_from(N, nb, sg), &t);
 }
 
 // The same with the adapters' part, which leaves a CU room for one workgroup.  Every
@@ -1018,9 +1057,6 @@ const LoraShape &best_lora(int64_t M, int64_t N, int32_t nb, int32_t sg) {
 }
 static_assert(kW4Rows == 32, "the rows of a tile");
 
-// slabs whose grids stay far below what a launch takes
-constexpr int64_t kSlabM = int64_t(1) << 18, kSlabN = int64_t(1) << 20;
-
 }  // namespace
 
 hipError_t launch_w4_pack(const W4Args &a, hipStream_t st) {
@@ -1074,6 +1110,8 @@ hipError_t launch_gemm_w4_lora(const W4GemmArgs &a, const W4Lora &l, hipStream_t
 hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs *plan) {
   const bool far = far_rows(all);
   if (plan && !gemm_w4_runs_plan(all)) return hipErrorInvalidValue;
+  // all slabs alike
+  const bool rounds = all.M >= rounded_from(std::min<int64_t>(all.N, kSlabN), all.nb, all.sg);
   for (int64_t m0 = 0; m0 < all.M; m0 += kSlabM)
     for (int64_t n0 = 0; n0 < all.N; n0 += kSlabN) {
       W4GemmArgs a = all;
@@ -1083,7 +1121,8 @@ hipError_t launch_gemm_w4(const W4GemmArgs &all, hipStream_t st, const PlanArgs 
       a.w += n0 / 16 * a.nb * w4_record(a.sg);
       a.y += m0 * a.ldy + n0;
       if (!far) {
-        best_of(a.M, a.N, a.nb, a.sg).launch(a, plan, st);
+        double t;
+        best_of(a.M, a.N, a.nb, a.sg, rounds, &t).launch(a, plan, st);
       } else {
         const dim3 grid((a.N + 15) / 16, (a.M + 15) / 16);
         if (a.sg == 1) hipLaunchKernelGGL(k_w4_far<1>, grid, dim3(256), 0, st, a);
