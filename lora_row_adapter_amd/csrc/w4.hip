@@ -1059,18 +1059,41 @@ static_assert(kW4Rows == 32, "the rows of a tile");
 
 }  // namespace
 
-hipError_t launch_w4_pack(const W4Args &a, hipStream_t st) {
-  const int64_t recs = (a.d + 15) / 16 * a.nb;
-  hipLaunchKernelGGL(k_w4_pack, dim3((unsigned)recs), dim3(256), 0, st, a);
-  return hipGetLastError();
+// A grid of 2^32 threads or more is cut off without an error: slabs of rows that
+// hold at most this many records (a row of records, 2^17 at most, always fits).
+static constexpr int64_t kSlabRecords = int64_t(1) << 22;
+
+hipError_t launch_w4_pack(const W4Args &all, hipStream_t st) {
+  const int64_t slab = kSlabRecords / all.nb * 16;
+  for (int64_t n0 = 0; n0 < all.d; n0 += slab) {
+    W4Args a = all;
+    a.d = std::min(slab, all.d - n0);
+    a.q += n0 * a.ldq;
+    a.scales = (const uint8_t *)a.scales + n0 * a.lds * (a.scale_dtype == 1 ? 2 : 4);
+    if (a.zeros) a.zeros += n0 * a.ldz;
+    a.w += n0 / 16 * a.nb * w4_record(a.sg);
+    hipLaunchKernelGGL(k_w4_pack, dim3((unsigned)((a.d + 15) / 16 * a.nb)), dim3(256), 0, st, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
-hipError_t launch_w4_dequantize(const W4Args &a, hipStream_t st) {
-  const int32_t per_row = (a.nb + kDqRecords - 1) / kDqRecords;
-  const dim3 grid((unsigned)((a.d + 15) / 16 * per_row));
-  if (a.dtype == 1) hipLaunchKernelGGL(k_w4_dequantize<uint16_t>, grid, dim3(256), 0, st, a, per_row);
-  else hipLaunchKernelGGL(k_w4_dequantize<float>, grid, dim3(256), 0, st, a, per_row);
-  return hipGetLastError();
+hipError_t launch_w4_dequantize(const W4Args &all, hipStream_t st) {
+  const int32_t per_row = (all.nb + kDqRecords - 1) / kDqRecords;
+  const int64_t slab = kSlabRecords / per_row * 16;
+  for (int64_t n0 = 0; n0 < all.d; n0 += slab) {
+    W4Args a = all;
+    a.d = std::min(slab, all.d - n0);
+    a.w += n0 / 16 * a.nb * w4_record(a.sg);
+    a.y = (uint8_t *)a.y + n0 * a.ldy * (a.dtype == 1 ? 2 : 4);
+    const dim3 grid((unsigned)((a.d + 15) / 16 * per_row));
+    if (a.dtype == 1) hipLaunchKernelGGL(k_w4_dequantize<uint16_t>, grid, dim3(256), 0, st, a, per_row);
+    else hipLaunchKernelGGL(k_w4_dequantize<float>, grid, dim3(256), 0, st, a, per_row);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]) {

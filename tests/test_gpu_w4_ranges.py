@@ -21,6 +21,11 @@ def _gpu():
     lr.load_library()
     yield
     torch.cuda.synchronize()
+
+
+@pytest.fixture(autouse=True)
+def _freed():
+    yield
     torch.cuda.empty_cache()  # the buffers here are of many GiB
 
 
@@ -55,3 +60,43 @@ def test_pages_past_32_bits():
                 y = lr.lora_linear_sliced_w4(x, Wp, [lr.Slice(d, a, sc) for d, a in zip(ds, ad)], ids_d)
                 want, _ = E.layer(x, dense, ds, sets, ranks, scales, ids, twice=M > 32)
                 assert torch.equal(y, want)
+
+
+def bytes_at_random(seed, *shape):
+    t = torch.empty(shape, dtype=torch.uint8, device="cuda")
+    t.view(-1).view(torch.int64).random_(generator=torch.Generator(device="cuda").manual_seed(seed))
+    return t
+
+
+def test_pack_past_a_launch():
+    """More records (2^24) than a launch has threads for: all as when 4096 rows
+    are laid out at a time."""
+    d, k, group, step = (1 << 18) + 16, 1 << 17, 128, 4096
+    say("w4 pack, %d records" % (d // 16 * k // 128))
+    q, z = bytes_at_random(1, d, k // 2), bytes_at_random(2, d, k // group)
+    s = (bytes_at_random(3, d, k // group).to(BF) - 100) / 64
+    W = lr.lora_w4_pack(q, s, k, group, zeros=z)
+    for r in range(0, d, step):
+        part = lr.lora_w4_pack(q[r:r + step], s[r:r + step], k, group, zeros=z[r:r + step])
+        at = r // 16 * (k // 128) * 1088
+        n = part.data.numel()
+        assert torch.equal(W.data[at:at + n], part.data)
+    last = lr.lora_w4_dequantize(part, F32)  # and by the definition
+    codes = torch.stack([q[r:] & 15, q[r:] >> 4], -1).flatten(1)
+    want = s[r:].float().repeat_interleave(group, 1) * (codes.float() - (z[r:] % 32).float().repeat_interleave(group, 1))
+    assert torch.equal(last, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_read_back_past_a_launch(dtype):
+    """As many rows as take 2^24 workgroups and three more."""
+    d, k, step = (1 << 28) + 48, 8, 1 << 24
+    say("w4 read back, %d rows, %s" % (d, dtype))
+    q = bytes_at_random(4, d, k // 2)
+    s = (bytes_at_random(5, d, 1).to(BF) - 100) / 64
+    W = lr.lora_w4_pack(q, s, k, 128)
+    y = lr.lora_w4_dequantize(W, dtype)
+    for r in range(0, d, step):
+        codes = torch.stack([q[r:r + step] & 15, q[r:r + step] >> 4], -1).flatten(1)
+        want = (s[r:r + step].float() * (codes.float() - 8)).to(dtype)  # 8 by 4 bits: exact in fp32
+        assert torch.equal(y[r:r + step], want)
