@@ -313,7 +313,8 @@ hipError_t launch_heads(const HeadsArgs &all, hipStream_t st) {
   int64_t rounds = std::min<int64_t>(64, (all.M * H + round * 1024 - 1) / (round * 1024));
   while (rounds > 1 && bytes(rounds * round) > 32768) --rounds;
 
-  const int64_t slab = std::max<int64_t>(1, (int64_t(1) << 30) / H);  // rows a launch
+  // rows a launch: a grid of 2^32 threads or more is cut off without an error
+  const int64_t slab = std::max<int64_t>(1, std::min<int64_t>(int64_t(1) << 30, (rounds * round) << 22) / H);
   for (int64_t m0 = 0; m0 < all.M; m0 += slab) {
     HeadsArgs a = all;
     a.M = std::min(slab, all.M - m0);

@@ -1,11 +1,13 @@
-"""The 4-bit weight and its layer at the ends of the ranges that the checks of
-arguments accept, bit for bit (w4_exact: every sum is exact)."""
+"""The 4-bit weight and its layer, and the heads behind it, at the ends of the
+ranges that the checks of arguments accept; the former bit for bit (w4_exact:
+every sum is exact)."""
 import numpy as np
 import pytest
 import torch
 
 import lora_row_adapter_amd as lr
 import w4_exact as E
+import w4_ref as R
 from gpu_helpers import say
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +102,29 @@ def test_read_back_past_a_launch(dtype):
         codes = torch.stack([q[r:r + step] & 15, q[r:r + step] >> 4], -1).flatten(1)
         want = (s[r:r + step].float() * (codes.float() - 8)).to(dtype)  # 8 by 4 bits: exact in fp32
         assert torch.equal(y[r:r + step], want)
+
+
+def test_heads_past_a_launch():
+    """As many heads, of a size that a workgroup takes four of, as take 2^24
+    workgroups and two more; in place.  Tolerance as in the heads' own tests."""
+    M, D, eps = (1 << 26) + 7, 912, 1e-6
+    say("heads, %d rows of %d" % (M, D))
+    q = torch.empty(M, 1, D, dtype=BF, device="cuda")
+    pos = torch.full((M,), -1, dtype=torch.int64, device="cuda")
+    at = torch.tensor([0, 5, (1 << 24) - 1, 1 << 24, (1 << 25) - 1, 1 << 25, (1 << 25) + 1, (1 << 26) - 1, 1 << 26, M - 1])
+    g = torch.Generator().manual_seed(6)
+    x = torch.randn(len(at), 1, D, generator=g).to(BF)
+    beside = at[:-1] + 1  # padding rows, left as they are
+    beside = beside[~torch.isin(beside, at)]
+    pad = torch.randn(len(beside), 1, D, generator=g).to(BF)
+    q[at.cuda()], q[beside.cuda()] = x.cuda(), pad.cuda()
+    p = torch.randint(0, 100000, (len(at),), generator=g)
+    pos[at.cuda()] = p.cuda()
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(BF)
+    inv = torch.tensor([1e4 ** (-2 * i / D) for i in range(D // 2)], dtype=F32)
+    lr.lora_qk_norm_rope(q, None, pos, lr.Rope(inv.cuda()), w.cuda(), eps=eps, q_out=q)
+    angle = p.double().numpy()[:, None] * inv.double().numpy()
+    want, mag = R.heads(x.double().numpy(), w.double().numpy(), eps, np.cos(angle), np.sin(angle), D, False)
+    got = q[at.cuda()].cpu().double().numpy()
+    assert (np.abs(got - want) <= 2.0 ** -21 * mag + 2.0 ** -8 * np.abs(want)).all()
+    assert torch.equal(q[beside.cuda()].cpu(), pad)
