@@ -116,6 +116,15 @@ lora_status_t lora_linear_sliced_w4(int64_t M, int64_t k, const void *x, int64_t
                                     int64_t ldy, void *workspace, size_t workspace_bytes,
                                     int32_t path, uint32_t flags, void *stream);
 
+/*
+ * Testing hook: which product lora_linear_sliced_w4 (but by LORA_PATH_GATHER)
+ * launches for 1 to 8192 rows without a given plan: of those that add the
+ * adapters' part, numbered first, or of lora_gemm_w4's (-1: invalid arguments).
+ * Host-only.  out[0], out[1]: the tile's rows of x and of W; out[2]: 1 where the
+ * plan is made in its launch.
+ */
+int32_t lora_test_linear_w4_shape(int64_t M, int64_t k, int64_t d, int32_t group, int32_t out[3]);
+
 #ifdef __cplusplus
 }
 #endif

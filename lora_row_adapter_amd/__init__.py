@@ -14,6 +14,6 @@ from ._binding import (  # noqa: F401
     status_str, workspace_bytes, workspace_bytes_sliced, gemm_workspace_bytes, test_sync_spin_limit,
     MX, MX_FP4, MX_FP8, Norm, test_gemm_mx_shape, lora_gemm_mx, lora_linear_sliced_mx, lora_mx_dequantize,
     lora_mx_quantize, lora_rmsnorm, workspace_bytes_sliced_mx,
-    W4, test_gemm_w4_shape, lora_gemm_w4, lora_linear_sliced_w4, lora_w4_dequantize, lora_w4_pack,
+    W4, test_gemm_w4_shape, test_linear_w4_shape, lora_gemm_w4, lora_linear_sliced_w4, lora_w4_dequantize, lora_w4_pack,
     workspace_bytes_sliced_w4, Rope, lora_qk_norm_rope,
 )

@@ -241,6 +241,8 @@ def load_library():
     lib.lora_gemm_w4.restype = i32
     lib.lora_test_gemm_w4_shape.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i32)]
     lib.lora_test_gemm_w4_shape.restype = i32
+    lib.lora_test_linear_w4_shape.argtypes = [i64, i64, i64, i32, ctypes.POINTER(i32)]
+    lib.lora_test_linear_w4_shape.restype = i32
     lib.lora_workspace_bytes_sliced_w4.argtypes = [i64, i64, i32, psl]
     lib.lora_workspace_bytes_sliced_w4.restype = sz
     lib.lora_linear_sliced_w4.argtypes = [i64, i64, p, i64, pw4, i32, psl, p, p, i64, p, sz, i32, u32, p]
@@ -1233,6 +1235,16 @@ def test_gemm_w4_shape(M: int, k: int, d: int, group: int):
     i = load_library().lora_test_gemm_w4_shape(int(M), int(k), int(d), int(group), out)
     if i < 0:
         raise LoraError(1, "lora_test_gemm_w4_shape")
+    return (i,) + tuple(out)
+
+
+def test_linear_w4_shape(M: int, k: int, d: int, group: int):
+    """Testing hook: (index, rows, columns, 1 if the plan is made in its launch)
+    of the product that lora_linear_sliced_w4 launches."""
+    out = (ctypes.c_int32 * 3)()
+    i = load_library().lora_test_linear_w4_shape(int(M), int(k), int(d), int(group), out)
+    if i < 0:
+        raise LoraError(1, "lora_test_linear_w4_shape")
     return (i,) + tuple(out)
 
 

@@ -299,6 +299,9 @@ bool gemm_w4_lora_runs_plan(const W4GemmArgs &a);
 // Index of the tile shape it takes; out: its rows, columns and whether it rounds
 // the weights to bf16.
 int gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t sg, int32_t out[3]);
+// The same of the product that the layer launches: those with the adapters' part
+// first, then the others; out[2]: whether the plan goes in its launch.
+int linear_w4_shape(const W4GemmArgs &a, int32_t out[3]);
 // Norm and rotation of heads (lora_heads.h).
 struct HeadSet {
   const void *x, *w;

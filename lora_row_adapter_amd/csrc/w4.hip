@@ -1122,6 +1122,20 @@ bool gemm_w4_lora_runs_plan(const W4GemmArgs &a) {
   return (a.N + bn - 1) / bn % 256 != 0;
 }
 
+int linear_w4_shape(const W4GemmArgs &a, int32_t out[3]) {
+  constexpr int kFew = sizeof(kLoraShapes) / sizeof(kLoraShapes[0]);
+  if (!gemm_w4_adds_lora(a)) {
+    const int i = gemm_w4_shape(a.M, a.K, a.N, a.sg, out);
+    out[2] = gemm_w4_runs_plan(a);
+    return kFew + i;
+  }
+  const LoraShape &s = best_lora(a.M, a.N, a.nb, a.sg);
+  out[0] = s.bm;
+  out[1] = s.bn;
+  out[2] = gemm_w4_lora_runs_plan(a);
+  return (int)(&s - kLoraShapes);
+}
+
 hipError_t launch_gemm_w4_lora(const W4GemmArgs &a, const W4Lora &l, hipStream_t st, const PlanArgs *plan) {
   if (!gemm_w4_adds_lora(a)) return hipErrorInvalidValue;
   LoraWith w{l, {}, plan != nullptr};

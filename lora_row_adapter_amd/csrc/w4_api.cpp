@@ -2,8 +2,6 @@
 // (the layer runs in lora_api.cpp's linear_sliced_impl).
 #include <hip/hip_runtime.h>
 
-#include <algorithm>
-
 #include "lora_w4.h"
 #include "kernels.hpp"
 #include "spans.hpp"
@@ -147,6 +145,12 @@ lora_status_t lora_gemm_w4(int64_t M, int64_t k, int64_t d, const void *x, int64
 int32_t lora_test_gemm_w4_shape(int64_t M, int64_t k, int64_t d, int32_t group, int32_t out[3]) {
   if (out == nullptr || M < 1 || lora_w4_bytes(d, k, group) == 0) return -1;
   return gemm_w4_shape(M, k, d, groups_in_record(group), out);
+}
+
+int32_t lora_test_linear_w4_shape(int64_t M, int64_t k, int64_t d, int32_t group, int32_t out[3]) {
+  if (out == nullptr || M < 1 || M > kPlanMaxRows || k % 8 || lora_w4_bytes(d, k, group) == 0) return -1;
+  const lora_w4_t W{group, nullptr};
+  return linear_w4_shape(make_w4_args(M, k, d, nullptr, k, &W, nullptr, d), out);
 }
 
 size_t lora_workspace_bytes_sliced_w4(int64_t max_rows, int64_t k, int32_t n_slices,
