@@ -52,9 +52,11 @@ typedef struct lora_rope {
  * q: not NULL; k, rope: may be NULL (no keys; norms alone).  All tensors but
  * positions and inv_freq are of `dtype` (F32 or BF16), aligned to their
  * elements; head_dim 1 .. 1024, n_heads 1 .. 65535, strides below 2^40;
- * rows and heads of a tensor must not overlap one another: ld_head >=
- * head_dim and ld_row >= (n_heads - 1) ld_head + head_dim (the first only
- * where n_heads > 1, the second where M > 1).  Sums of squares and angles
+ * rows and heads of a tensor must not overlap one another: ld_head, ld_row >=
+ * head_dim, and ld_row >= (n_heads - 1) ld_head + head_dim (all heads of a row,
+ * then the next row) or ld_head >= (M - 1) ld_row + head_dim (all rows of a
+ * head, then the next head); ld_head counts only where n_heads > 1, ld_row
+ * where M > 1.  Sums of squares and angles
  * are computed in 64 bits, the values in fp32 (two roundings of the norm, three
  * of the rotation); each output is rounded once from there.  A row whose
  * position is negative (padding) is left as it is in both outputs.  The

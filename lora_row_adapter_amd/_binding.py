@@ -1146,9 +1146,6 @@ class W4:
             raise LoraError(2, "lora_w4_bytes")
         return n
 
-    def ref(self):
-        return self._ref
-
 
 def lora_w4_pack(q: torch.Tensor, scales: torch.Tensor, k: int, group: int,
                  zeros: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,

@@ -32,7 +32,9 @@ __device__ __forceinline__ bf16x8_t codes(uint32_t w) {
 }
 
 // ---------------------------------------------------------------- layout
-// One workgroup a record: 256 threads a dword of codes each, then its scales.
+// One workgroup a record: 256 threads a dword of codes each, then its scales.  Done
+// once for a weight, so codes are read byte by byte, as any alignment of theirs
+// allows: 9216 x 8192 70 us, 1.1 TB/s.
 __global__ __launch_bounds__(256) void k_w4_pack(W4Args a) {
   const int64_t rec = blockIdx.x, tile = rec / a.nb, blk = rec - tile * a.nb;
   uint32_t *out = reinterpret_cast<uint32_t *>(a.w + rec * w4_record(a.sg));
@@ -74,7 +76,8 @@ __global__ __launch_bounds__(256) void k_w4_pack(W4Args a) {
 // A workgroup reads kDqRecords records of 16 rows back; of each, a thread takes
 // a dword of codes (eight columns of a row) and sixteen threads a row's 128
 // columns.  All of a thread's loads go ahead of its stores.  Bound by its bytes:
-// 9216 x 8192 to bf16 45 us, 4.2 TB/s.
+// 9216 x 8192 to bf16 37 - 45 us, 4.2 TB/s and more (a part stays in the last-level
+// cache), to fp32 102 us, 3.4 TB/s (a thread's 32 bytes are two stores).
 constexpr int kDqRecords = 8;
 template <typename T>
 __global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, int32_t per_row) {
@@ -121,7 +124,9 @@ __global__ __launch_bounds__(256) void k_w4_dequantize(W4Args a, int32_t per_row
 // ---------------------------------------------------------------- few rows
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
-constexpr uint32_t kOob = 0xFFFFFFF0u;  // past every buffer: loads give zeros
+// Past every buffer: loads give zeros.  Either offset may be it: the two are added
+// without wrapping (read back on the machine, from a buffer that goes on).
+constexpr uint32_t kOob = 0xFFFFFFF0u;
 
 __device__ __forceinline__ bf16x8_t ones8() {
   return __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
@@ -369,10 +374,11 @@ struct LoraPart {
 // Loads past the end of a wave's records, of x's rows and of its columns are
 // past their buffer: they move nothing and give zeros.
 //
-// 1 x 9216 x 8192, groups of 128: 8.5 us, bound by W's bytes (4.7 TB/s, most of them from
-// the last-level cache); 7 x 4999 x 5000, groups of 32: 7.0, its records' latencies
-// one after the other; 256 x 4096 x 4096: 15.2, unpacking and scaling between the products
-// (matrix units busy 32%).  Eight waves a tile: sixteen took the same within 1%.
+// 1 x 9216 x 8192, groups of 128: 8.4 us, bound by W's bytes (4.7 TB/s, most of them from
+// the last-level cache; 16 weights in turn, from HBM: 10.6, 3.75 TB/s); 7 x 4999 x 5000,
+// groups of 32: 7.0, its records' latencies one after the other; 256 x 4096 x 4096: 16.0,
+// unpacking and scaling between the products (matrix units busy 32%).  Eight waves a
+// tile: sixteen took the same within 1%.
 template <int FM, int FN, int NW, int PD, int SG, With kWith>
 __global__ __launch_bounds__(64 * (NW + (kWith == kLora ? lora_waves<FM, FN> : 0))) void k_w4_split(W4GemmArgs p,
                                                                                               with_t<kWith> with) {
@@ -658,7 +664,7 @@ struct WTile {
   static_assert((ST - 1) * XL + ST / 2 * WL < 64, "vmcnt");
 };
 
-// 8192 x 4096 x 4096 (groups of 64, 256 x 256 tiles): 236 us, 1.16 PFLOP/s, against 202
+// 8192 x 4096 x 4096 (groups of 64, 256 x 256 tiles): 233 us, 1.18 PFLOP/s, against 202
 // at the library's bf16 rate; 512 x 9216 x 8192 (groups of 128, 128 x 160): 85 - 95.  Unpacking
 // bounds both: it takes issue slots that other waves' matrix instructions do not
 // fill (two VALU instructions behind one are free, a third takes a quarter of it more).

@@ -11,8 +11,9 @@
 // in: 64 bytes a clock where a wave's load is one run of memory, as here (each lane
 // eight columns of one row of A), a quarter of that where it is 16 rows of 64 bytes,
 // as matrix instructions would have it.  At two slices of 64 ranks x 8192: one row
-// 4.5 us (2.2 of them the launch and the rows' checks; 10.5 with matrix instructions and
-// all of k to a workgroup), 16 rows of 12 adapters 7.5 (25 MB of A).
+// 4.6 us, 2.2 MB of A (4.4 with 8 ranks; 2.2 of them the launch and the rows' checks;
+// 10.5 with matrix instructions and all of k to a workgroup); 16 rows of 12 adapters
+// 9.1 us, 26 MB; of 8 adapters of 4 to 64 ranks 7.4 us, 8.5 MB.
 #include <algorithm>
 
 #include "kernels.hpp"
