@@ -73,7 +73,7 @@ lora_status_t lora_w4_dequantize(lora_dtype_t dtype, int64_t d, int64_t k, const
 /*
  * y = x W^T: x bf16 [M, k] (k, ldx multiples of 8, 16-byte aligned), y bf16
  * [M, d] (ldy >= d).  Up to a number of rows that the weight's sizes alone set
- * (32 at least, 64 to some hundred for a model's: lora_test_gemm_w4_shape)
+ * (32 at least, up to some hundred for a model's: lora_test_gemm_w4_shape)
  * codes meet x exactly, and each group's sum is scaled and added in fp32; past
  * it the weights are rounded to bf16, once each (by 2^-8 of a weight at most),
  * ahead of the product.  y is rounded once.  Sums that leave fp32's range on the
